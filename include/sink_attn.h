@@ -47,7 +47,8 @@
  *     (fp32), cu_seqlens [batch+1] (int32, device, cu_seqlens[0] = 0,
  *     cu_seqlens[batch] = T, non-decreasing).
  *   - Supported: D = 64; Hq % Hkv == 0 with G = Hq / Hkv a power of two
- *     <= 128; scale finite and > 0; bf16 tensors 16-byte aligned.
+ *     <= 128 (any whole number <= 128 over a paged cache); scale finite and
+ *     > 0; bf16 tensors 16-byte aligned.
  *   - A device-side wait that exceeds its time limit (about one second; it
  *     never happens in a correct build) makes the kernel record an error
  *     code and return instead of hanging; sink_attn_last_device_error()
@@ -312,6 +313,152 @@ sink_attn_status sink_attn_decode_e4m3_f8pv(const sink_attn_decode_dims* dims,
  * combine, or only the first two when one CTA per (sequence, key/value head)
  * covers the cache (the attend kernel then finishes the rows itself). */
 int sink_attn_decode_launches(const sink_attn_decode_dims* dims, int window);
+
+/* ------------------------------------------------------------- paged cache
+ * Serving over a paged key/value cache: the keys and values of all requests
+ * live in a pool of num_pages pages of page_size tokens each, and a request
+ * owns the pages its row of block_table names.  A serving step is
+ *
+ *   sink_attn_paged_plan    lengths -> block-table entries, slots, cu_seqlens
+ *   sink_attn_paged_append  the new keys and values into their slots (per layer)
+ *   sink_attn_paged_attn    the new tokens' attention over the pages (per layer)
+ *
+ * It is the paged counterpart of the "Dynamic Sliding Window Layer & Cache" of
+ * "Tricks from OpenAI gpt-oss you can use with transformers": the pages do not
+ * describe a paged cache, so its layout is this library's own.
+ *
+ *   - k_cache / v_cache hold [num_pages][page_size][Hkv][D] elements, bf16 or
+ *     e4m3 codes, at any strides (in elements, the same for both): the D
+ *     elements of a row are contiguous, rows are 16-byte aligned.  Token-major
+ *     pages, head-major pages and the two halves of one fused tensor are all
+ *     given by their strides.
+ *   - The token at position p of request b lies in page
+ *     block_table[b][p / page_size] at offset p mod page_size; its slot is
+ *     page * page_size + offset (int32; num_pages * page_size < 2^31).
+ *     Entries of pages that no query of a call can see are not read and may
+ *     hold anything, -1 for example; slots that hold no visible token may hold
+ *     any bits, NaN included.
+ *   - The new tokens of a step are packed: request b's are rows
+ *     cu_seqlens[b] .. cu_seqlens[b+1] - 1 of q.  kv_lens[b] counts its tokens
+ *     after the step, so its new token t has position
+ *     kv_lens[b] - (cu_seqlens[b+1] - cu_seqlens[b]) + t.
+ *   - page_size is a power of two from 16 to 1024.
+ *   - What only the device can see (a page outside the pool, lengths that do
+ *     not fit) never leads to an access out of range: it is recorded as a
+ *     device error (0x202 the pool ran dry, 0x203 a page outside the pool,
+ *     0x204 lengths that do not fit the table or the slot map, 0x205 rows
+ *     that do not fit total_tokens or max_new), see sink_attn_device_error().
+ */
+
+/* Planning a step.  One launch; nothing is read back to the host, so a step
+ * can be captured into a CUDA graph and replayed with new lengths.
+ *
+ * In: cached_lens [batch] (tokens in the cache before the step), new_lens
+ * [batch] (new tokens; 0: idle; negative: the request has ended), pool = {head,
+ * count}: the free pages are free_pages[(head + i) mod num_pages], i < count,
+ * first_page [batch] or NULL (leading pages of the request that it gave back
+ * earlier).  In and out: block_table [batch][max_pages], free_pages
+ * [num_pages].  Out: cu_seqlens [batch + 1], kv_lens [batch], slot_map
+ * [max_tokens], pool_out (2 ints), first_page_out [batch] (NULL with
+ * first_page).  All int32, 4-byte aligned.
+ *
+ *   - Request b needs ceil((c + n) / P) - ceil(c / P) new pages; they are taken
+ *     from the head of the ring in the order of the requests and written to its
+ *     table row.  A request that needs pages when those left do not suffice
+ *     gets none, nor does any request behind it that needs some: its slots are
+ *     -1, its kv_lens stays cached_lens, and device error 0x202 is recorded.
+ *   - An ended request gives back its pages (from first_page on); its kv_lens
+ *     and first_page_out become 0.
+ *   - With window > 0 (needs first_page) a request gives back the pages wholly
+ *     before position cached_lens - window + 1, which no query of this step or
+ *     a later one sees.  Pages given back go to the tail of the ring, in the
+ *     order of requests and pages; this step takes none of them.
+ *   - slot_map[t] is the slot of packed token t, and -1 from the last token on
+ *     up to max_tokens.
+ *   - kv_lens may be cached_lens, pool_out may be pool and first_page_out may
+ *     be first_page; other overlaps are not allowed.  Where they are distinct,
+ *     the call can be repeated and gives the same again.
+ *
+ * batch is at most 4096.  batch = 0 is a no-op. */
+typedef struct {
+    int batch;      /* requests */
+    int max_tokens; /* entries of slot_map */
+    int max_pages;  /* entries of a block-table row */
+    int page_size;
+    int num_pages;  /* pages of the pool, entries of free_pages */
+} sink_attn_plan_dims;
+
+sink_attn_status sink_attn_paged_plan(const sink_attn_plan_dims* dims,
+                                      const int* cached_lens, const int* new_lens,
+                                      int* block_table, int* free_pages, const int* pool,
+                                      const int* first_page, int window,
+                                      int* cu_seqlens, int* kv_lens, int* slot_map,
+                                      int* pool_out, int* first_page_out, void* stream);
+
+typedef struct {
+    int batch;        /* requests (attention only) */
+    int total_tokens; /* T: rows of q / out, or of k_new / v_new and slot_map */
+    int max_new;      /* attention only: >= the new tokens of every request */
+    int num_q_heads;  /* Hq (attention only) */
+    int num_kv_heads; /* Hkv */
+    int head_dim;     /* D (64) */
+    int page_size;
+    int num_pages;
+    int max_pages;         /* entries of a block-table row (attention only) */
+    long long page_stride; /* strides of k_cache and v_cache, in elements */
+    long long token_stride;
+    long long head_stride;
+    long long q_stride;    /* elements between tokens of q (attention only) */
+} sink_attn_paged_dims;
+
+/* Appends new keys and values: row t of k_new / v_new ([T][Hkv][D] bf16, k_stride
+ * and v_stride elements between tokens) goes to slot slot_map[t]; a negative
+ * slot is skipped.  If a slot occurs twice, which of its tokens it holds
+ * afterwards is not defined.  T = 0 is a no-op. */
+sink_attn_status sink_attn_paged_append(const sink_attn_paged_dims* dims,
+                                        const void* k_new, const void* v_new,
+                                        long long k_stride, long long v_stride, const int* slot_map,
+                                        void* k_cache, void* v_cache, void* stream);
+
+/* The same into an e4m3 cache: code = e4m3(x * (1 / scale)), rounded to nearest
+ * even and saturated to +-448, with one scale per key/value head (fp32 [Hkv],
+ * device, > 0). */
+sink_attn_status sink_attn_paged_append_e4m3(const sink_attn_paged_dims* dims,
+                                             const void* k_new, const void* v_new,
+                                             long long k_stride, long long v_stride, const int* slot_map,
+                                             void* k_cache, void* v_cache,
+                                             const float* k_scale, const float* v_scale, void* stream);
+
+/* Bytes of device workspace sink_attn_paged_attn() and its e4m3 form need (0
+ * when the sizes are invalid). */
+size_t sink_attn_paged_workspace_size(const sink_attn_paged_dims* dims);
+
+/* Attention of a step's new tokens, one or many per request, over the paged
+ * cache: the forward's operation (sink, window, causal order by position).
+ * q [T][Hq][D] bf16 (q_stride elements between tokens), block_table
+ * [batch][max_pages], cu_seqlens [batch + 1] and kv_lens [batch] (int32,
+ * device), sinks [Hq] fp32.  Writes out [T][Hq][D] bf16 (dense) and lse
+ * [Hq][T] fp32 of the rows before cu_seqlens[batch]; rows behind them are left
+ * as they were.  A row that sees no key gets out = 0 and lse = its sink.
+ * G = Hq / Hkv is any whole number up to 128.  `workspace`: caller-owned,
+ * 256-byte aligned, of sink_attn_paged_workspace_size(dims) bytes; calls whose
+ * execution may overlap need one each.  T = 0 or batch = 0 is a no-op. */
+sink_attn_status sink_attn_paged_attn(const sink_attn_paged_dims* dims,
+                                      const void* q, const void* k_cache, const void* v_cache,
+                                      const int* block_table, const int* cu_seqlens, const int* kv_lens,
+                                      const float* sinks, int window, float scale,
+                                      void* out, float* lse,
+                                      void* workspace, size_t workspace_bytes, void* stream);
+
+/* The same over e4m3 codes: key = code * k_scale[g], value = code * v_scale[g]
+ * (fp32 [Hkv], device, > 0). */
+sink_attn_status sink_attn_paged_attn_e4m3(const sink_attn_paged_dims* dims,
+                                           const void* q, const void* k_cache, const void* v_cache,
+                                           const int* block_table, const int* cu_seqlens, const int* kv_lens,
+                                           const float* k_scale, const float* v_scale,
+                                           const float* sinks, int window, float scale,
+                                           void* out, float* lse,
+                                           void* workspace, size_t workspace_bytes, void* stream);
 
 /* Human-readable name of a status code (static string, never NULL). */
 const char* sink_attn_status_string(sink_attn_status s);

@@ -1,0 +1,71 @@
+// Writing a step's new keys and values into a paged cache: token t's rows of
+// k_new / v_new go to slot_map[t] = page * page_size + offset, in bf16 or as
+// e4m3 codes.  A pure copy, bound by HBM: every byte is read and written once.
+#pragma once
+#include "decode_kernel.cuh"
+
+namespace sa {
+
+struct AppendParams {
+  int tokens, Hkv;
+  int page_log2;
+  long long slots_end;                            // num_pages * page_size
+  long long k_stride, v_stride;                   // elements between tokens of k_new / v_new
+  long long page_stride, token_stride, head_stride;  // elements of the caches
+  const int* slots;
+  const __nv_bfloat16* k_new;
+  const __nv_bfloat16* v_new;
+  void* k_cache;
+  void* v_cache;
+  const float* k_scale;  // e4m3: [Hkv]
+  const float* v_scale;
+};
+
+// One thread per 16 elements of a key row and of the value row beside it.
+template <bool kF8>
+__global__ void __launch_bounds__(256) sink_attn_paged_append_kernel(const AppendParams p) {
+  constexpr int kChunks = kHeadDim / 16;
+  const long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
+  const int per = p.Hkv * kChunks;
+  const long long t = i / per;
+  if (t >= p.tokens) return;
+  const int r = static_cast<int>(i - t * per);
+  const int g = r / kChunks, c = r % kChunks;
+  const int slot = __ldg(p.slots + t);
+  if (slot < 0) return;  // padding, or a request without room
+  if (slot >= p.slots_end) {
+    atomicCAS(&g_device_error, 0, static_cast<int>(kDevErrBadPage));
+    return;
+  }
+  const uint4* ks = reinterpret_cast<const uint4*>(p.k_new + t * p.k_stride + g * kHeadDim + c * 16);
+  const uint4* vs = reinterpret_cast<const uint4*>(p.v_new + t * p.v_stride + g * kHeadDim + c * 16);
+  const uint4 k0 = __ldg(ks), k1 = __ldg(ks + 1), v0 = __ldg(vs), v1 = __ldg(vs + 1);
+  const long long dst = (slot >> p.page_log2) * p.page_stride +
+                        (slot & ((1 << p.page_log2) - 1)) * p.token_stride + g * p.head_stride + c * 16;
+  if constexpr (kF8) {
+    const float ki = 1.f / __ldg(p.k_scale + g), vi = 1.f / __ldg(p.v_scale + g);
+    const uint32_t kin[8] = {k0.x, k0.y, k0.z, k0.w, k1.x, k1.y, k1.z, k1.w};
+    const uint32_t vin[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+    uint32_t kw[8], vw[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&kin[u]));
+      const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&vin[u]));
+      kw[u] = f32x2_to_e4m3x2(a.x * ki, a.y * ki);
+      vw[u] = f32x2_to_e4m3x2(b.x * vi, b.y * vi);
+    }
+    *reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.k_cache) + dst) =
+        make_uint4(kw[0] | (kw[1] << 16), kw[2] | (kw[3] << 16), kw[4] | (kw[5] << 16), kw[6] | (kw[7] << 16));
+    *reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.v_cache) + dst) =
+        make_uint4(vw[0] | (vw[1] << 16), vw[2] | (vw[3] << 16), vw[4] | (vw[5] << 16), vw[6] | (vw[7] << 16));
+  } else {
+    uint4* kd = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.k_cache) + dst);
+    uint4* vd = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.v_cache) + dst);
+    kd[0] = k0;
+    kd[1] = k1;
+    vd[0] = v0;
+    vd[1] = v1;
+  }
+}
+
+}  // namespace sa

@@ -18,6 +18,9 @@
 #include "fwd_pair_kernel.cuh"
 #include "bwd_kernels.cuh"
 #include "decode_kernel.cuh"
+#include "paged_plan.cuh"
+#include "paged_append.cuh"
+#include "paged_attn.cuh"
 
 namespace sa {
 namespace {
@@ -570,6 +573,242 @@ sink_attn_status sink_attn_decode_e4m3_f8pv(const sink_attn_decode_dims* d, cons
                                             void* workspace, size_t workspace_bytes, void* stream) {
   return decode_impl(d, q, k_new, v_new, k_cache, v_cache, cache_seqlens, k_scale, v_scale, 2, sinks, window,
                      scale, out, lse, workspace, workspace_bytes, stream);
+}
+
+}  // extern "C"
+
+// ----------------------------------------------------------------------------
+// Paged cache.
+namespace {
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// Sizes and strides shared by the paged append and attention.  `codes`: the
+// cache holds one byte per element, so a row's 16-byte alignment needs strides
+// that are multiples of 16 elements, not 8.
+sink_attn_status check_paged(const sink_attn_paged_dims* d, bool codes) {
+  if (!d) return SINK_ATTN_ERR_NULL;
+  if (d->total_tokens < 0 || d->num_kv_heads <= 0 || d->head_dim <= 0 || d->page_size <= 0 || d->num_pages <= 0 ||
+      d->page_stride < 0 || d->token_stride < 0 || d->head_stride < 0)
+    return SINK_ATTN_ERR_SHAPE;
+  if (d->head_dim != kHeadDim) return SINK_ATTN_ERR_UNSUPPORTED;
+  if (ilog2_exact(d->page_size) < 4 || d->page_size > 1024) return SINK_ATTN_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(d->num_pages) * d->page_size >= (int64_t(1) << 31) ||
+      d->total_tokens > (1 << 30) || d->num_kv_heads > (1 << 16))
+    return SINK_ATTN_ERR_UNSUPPORTED;
+  const long long unit = codes ? 16 : 8;
+  if (d->page_stride % unit || d->token_stride % unit || d->head_stride % unit) return SINK_ATTN_ERR_ALIGN;
+  return SINK_ATTN_OK;
+}
+
+sink_attn_status paged_append_impl(const sink_attn_paged_dims* d, const void* k_new, const void* v_new,
+                                   long long k_stride, long long v_stride, const int* slot_map, void* k_cache,
+                                   void* v_cache, const float* k_scale, const float* v_scale, bool codes,
+                                   void* stream) {
+  sink_attn_status st = check_paged(d, codes);
+  if (st != SINK_ATTN_OK) return st;
+  if (k_stride < 0 || v_stride < 0) return SINK_ATTN_ERR_SHAPE;
+  if (d->total_tokens == 0) return SINK_ATTN_OK;
+  if (!k_new || !v_new || !slot_map || !k_cache || !v_cache || (codes && (!k_scale || !v_scale)))
+    return SINK_ATTN_ERR_NULL;
+  if (!aligned16(k_new) || !aligned16(v_new) || !aligned16(k_cache) || !aligned16(v_cache) || k_stride % 8 ||
+      v_stride % 8 || !aligned4(slot_map) || !aligned4(k_scale) || !aligned4(v_scale))
+    return SINK_ATTN_ERR_ALIGN;
+  AppendParams p;
+  p.tokens = d->total_tokens;
+  p.Hkv = d->num_kv_heads;
+  p.page_log2 = ilog2_exact(d->page_size);
+  p.slots_end = static_cast<long long>(d->num_pages) * d->page_size;
+  p.k_stride = k_stride;
+  p.v_stride = v_stride;
+  p.page_stride = d->page_stride;
+  p.token_stride = d->token_stride;
+  p.head_stride = d->head_stride;
+  p.slots = slot_map;
+  p.k_new = static_cast<const __nv_bfloat16*>(k_new);
+  p.v_new = static_cast<const __nv_bfloat16*>(v_new);
+  p.k_cache = k_cache;
+  p.v_cache = v_cache;
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  const long long work = static_cast<long long>(p.tokens) * p.Hkv * (kHeadDim / 16);
+  const long long blocks = (work + 255) / 256;
+  if (blocks > 0x7fffffff) return SINK_ATTN_ERR_UNSUPPORTED;
+  cudaStream_t st_ = static_cast<cudaStream_t>(stream);
+  if (codes) sink_attn_paged_append_kernel<true><<<static_cast<unsigned>(blocks), 256, 0, st_>>>(p);
+  else sink_attn_paged_append_kernel<false><<<static_cast<unsigned>(blocks), 256, 0, st_>>>(p);
+  return cudaPeekAtLastError() == cudaSuccess ? SINK_ATTN_OK : SINK_ATTN_ERR_CUDA;
+}
+
+sink_attn_status check_paged_attn(const sink_attn_paged_dims* d, bool codes) {
+  sink_attn_status st = check_paged(d, codes);
+  if (st != SINK_ATTN_OK) return st;
+  if (d->batch < 0 || d->max_new <= 0 || d->max_pages <= 0 || d->num_q_heads <= 0 || d->q_stride < 0)
+    return SINK_ATTN_ERR_SHAPE;
+  if (d->num_q_heads % d->num_kv_heads != 0) return SINK_ATTN_ERR_SHAPE;
+  if (d->num_q_heads / d->num_kv_heads > kBlockM) return SINK_ATTN_ERR_UNSUPPORTED;
+  // Positions are 32-bit, with room for a tile behind the last one.
+  if (static_cast<int64_t>(d->max_pages) * d->page_size > (int64_t(1) << 30) || d->batch > (1 << 24))
+    return SINK_ATTN_ERR_UNSUPPORTED;
+  if (d->q_stride % 8) return SINK_ATTN_ERR_ALIGN;
+  return SINK_ATTN_OK;
+}
+
+sink_attn_status paged_attn_impl(const sink_attn_paged_dims* d, const void* q, const void* k_cache,
+                                 const void* v_cache, const int* block_table, const int* cu_seqlens,
+                                 const int* kv_lens, const float* k_scale, const float* v_scale, bool codes,
+                                 const float* sinks, int window, float scale, void* out, float* lse,
+                                 void* workspace, size_t workspace_bytes, void* stream) {
+  sink_attn_status st = check_paged_attn(d, codes);
+  if (st != SINK_ATTN_OK) return st;
+  if (!(scale > 0.f) || !std::isfinite(scale)) return SINK_ATTN_ERR_UNSUPPORTED;
+  if (d->total_tokens == 0 || d->batch == 0) return SINK_ATTN_OK;
+  if (!q || !k_cache || !v_cache || !block_table || !cu_seqlens || !kv_lens || !sinks || !out || !lse ||
+      (codes && (!k_scale || !v_scale)))
+    return SINK_ATTN_ERR_NULL;
+  if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out) || !aligned4(block_table) ||
+      !aligned4(cu_seqlens) || !aligned4(kv_lens) || !aligned4(sinks) || !aligned4(lse) || !aligned4(k_scale) ||
+      !aligned4(v_scale))
+    return SINK_ATTN_ERR_ALIGN;
+  if (workspace_bytes < sink_attn_paged_workspace_size(d) || !workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u))
+    return SINK_ATTN_ERR_WORKSPACE;
+  PagedParams p;
+  p.batch = d->batch;
+  p.T = d->total_tokens;
+  p.Hq = d->num_q_heads;
+  p.Hkv = d->num_kv_heads;
+  p.G = p.Hq / p.Hkv;
+  p.max_new = d->max_new;
+  p.page_log2 = ilog2_exact(d->page_size);
+  p.num_pages = d->num_pages;
+  p.max_pages = d->max_pages;
+  p.window = window > 0 ? window : 0;
+  p.scale_log2 = scale * kLog2e;
+  p.q_stride = d->q_stride;
+  p.page_stride = d->page_stride;
+  p.token_stride = d->token_stride;
+  p.head_stride = d->head_stride;
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.k_cache = k_cache;
+  p.v_cache = v_cache;
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  p.table = block_table;
+  p.cu = cu_seqlens;
+  p.kv_lens = kv_lens;
+  p.sinks = sinks;
+  p.out = static_cast<__nv_bfloat16*>(out);
+  p.lse = lse;
+  const long long rows = static_cast<long long>(p.T) * p.G;
+  if ((rows + 127) / 128 > 0x7fffffff || p.Hkv > 65535) return SINK_ATTN_ERR_UNSUPPORTED;
+  const dim3 grid(static_cast<unsigned>((rows + 127) / 128), static_cast<unsigned>(p.Hkv));
+  cudaStream_t st_ = static_cast<cudaStream_t>(stream);
+  if (codes) sink_attn_paged_kernel<true><<<grid, 128, 0, st_>>>(p);
+  else sink_attn_paged_kernel<false><<<grid, 128, 0, st_>>>(p);
+  return cudaPeekAtLastError() == cudaSuccess ? SINK_ATTN_OK : SINK_ATTN_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" {
+
+sink_attn_status sink_attn_paged_plan(const sink_attn_plan_dims* d, const int* cached_lens, const int* new_lens,
+                                      int* block_table, int* free_pages, const int* pool, const int* first_page,
+                                      int window, int* cu_seqlens, int* kv_lens, int* slot_map, int* pool_out,
+                                      int* first_page_out, void* stream) {
+  if (!d) return SINK_ATTN_ERR_NULL;
+  if (d->batch < 0 || d->max_tokens < 0 || d->max_pages <= 0 || d->page_size <= 0 || d->num_pages <= 0)
+    return SINK_ATTN_ERR_SHAPE;
+  if (ilog2_exact(d->page_size) < 4 || d->page_size > 1024 || d->batch > kPlanMaxBatch)
+    return SINK_ATTN_ERR_UNSUPPORTED;
+  // Slots, positions and their sums over the requests are 32-bit.
+  if (static_cast<int64_t>(d->num_pages) * d->page_size >= (int64_t(1) << 31) ||
+      static_cast<int64_t>(std::max(d->batch, 1)) * d->max_pages * d->page_size > (int64_t(1) << 30) ||
+      d->max_tokens > (1 << 30))
+    return SINK_ATTN_ERR_UNSUPPORTED;
+  // Giving pages back needs the record of those already given back.
+  if (window > 0 && !first_page) return SINK_ATTN_ERR_NULL;
+  if ((first_page == nullptr) != (first_page_out == nullptr)) return SINK_ATTN_ERR_NULL;
+  if (d->batch == 0) return SINK_ATTN_OK;
+  if (!cached_lens || !new_lens || !block_table || !free_pages || !pool || !cu_seqlens || !kv_lens || !pool_out ||
+      (d->max_tokens > 0 && !slot_map))
+    return SINK_ATTN_ERR_NULL;
+  if (!aligned4(cached_lens) || !aligned4(new_lens) || !aligned4(block_table) || !aligned4(free_pages) ||
+      !aligned4(pool) || !aligned4(first_page) || !aligned4(cu_seqlens) || !aligned4(kv_lens) ||
+      !aligned4(slot_map) || !aligned4(pool_out) || !aligned4(first_page_out))
+    return SINK_ATTN_ERR_ALIGN;
+  PlanParams p;
+  p.batch = d->batch;
+  p.max_tokens = d->max_tokens;
+  p.max_pages = d->max_pages;
+  p.page_size = d->page_size;
+  p.num_pages = d->num_pages;
+  p.page_log2 = ilog2_exact(d->page_size);
+  p.window = window > 0 ? window : 0;
+  p.cached = cached_lens;
+  p.fresh = new_lens;
+  p.table = block_table;
+  p.ring = free_pages;
+  p.pool = pool;
+  p.first = first_page;
+  p.cu = cu_seqlens;
+  p.kv = kv_lens;
+  p.slots = slot_map;
+  p.pool_out = pool_out;
+  p.first_out = first_page_out;
+  const size_t smem = plan_smem_bytes(p.batch);
+  static SmemAttrOnce smem_set;
+  if (!smem_set.ensure(sink_attn_paged_plan_kernel, plan_smem_bytes(kPlanMaxBatch))) return SINK_ATTN_ERR_CUDA;
+  const unsigned blocks = p.max_tokens > kPlanThreads ? 8 : 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(blocks, 1, 1);
+  cfg.blockDim = dim3(kPlanThreads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = blocks;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, sink_attn_paged_plan_kernel, p) == cudaSuccess ? SINK_ATTN_OK : SINK_ATTN_ERR_CUDA;
+}
+
+sink_attn_status sink_attn_paged_append(const sink_attn_paged_dims* d, const void* k_new, const void* v_new,
+                                        long long k_stride, long long v_stride, const int* slot_map, void* k_cache,
+                                        void* v_cache, void* stream) {
+  return paged_append_impl(d, k_new, v_new, k_stride, v_stride, slot_map, k_cache, v_cache, nullptr, nullptr, false,
+                           stream);
+}
+
+sink_attn_status sink_attn_paged_append_e4m3(const sink_attn_paged_dims* d, const void* k_new, const void* v_new,
+                                             long long k_stride, long long v_stride, const int* slot_map,
+                                             void* k_cache, void* v_cache, const float* k_scale, const float* v_scale,
+                                             void* stream) {
+  return paged_append_impl(d, k_new, v_new, k_stride, v_stride, slot_map, k_cache, v_cache, k_scale, v_scale, true,
+                           stream);
+}
+
+size_t sink_attn_paged_workspace_size(const sink_attn_paged_dims* d) {
+  return check_paged_attn(d, false) == SINK_ATTN_OK ? 256 : 0;
+}
+
+sink_attn_status sink_attn_paged_attn(const sink_attn_paged_dims* d, const void* q, const void* k_cache,
+                                      const void* v_cache, const int* block_table, const int* cu_seqlens,
+                                      const int* kv_lens, const float* sinks, int window, float scale, void* out,
+                                      float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+  return paged_attn_impl(d, q, k_cache, v_cache, block_table, cu_seqlens, kv_lens, nullptr, nullptr, false, sinks,
+                         window, scale, out, lse, workspace, workspace_bytes, stream);
+}
+
+sink_attn_status sink_attn_paged_attn_e4m3(const sink_attn_paged_dims* d, const void* q, const void* k_cache,
+                                           const void* v_cache, const int* block_table, const int* cu_seqlens,
+                                           const int* kv_lens, const float* k_scale, const float* v_scale,
+                                           const float* sinks, int window, float scale, void* out, float* lse,
+                                           void* workspace, size_t workspace_bytes, void* stream) {
+  return paged_attn_impl(d, q, k_cache, v_cache, block_table, cu_seqlens, kv_lens, k_scale, v_scale, true, sinks,
+                         window, scale, out, lse, workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"

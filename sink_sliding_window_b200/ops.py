@@ -28,7 +28,9 @@ STATUS = {
 EXPORTS = ("sink_attn_fwd", "sink_attn_fwd_pair", "sink_attn_fwd_with", "sink_attn_fwd_kernel_for", "sink_attn_bwd", "sink_attn_bwd_workspace_size", "sink_attn_status_string",
            "sink_attn_last_device_error", "sink_attn_device_error", "sink_attn_fwd_launches", "sink_attn_bwd_launches", "sink_attn_profile_events",
            "sink_attn_decode", "sink_attn_decode_workspace_size", "sink_attn_decode_launches",
-           "sink_attn_decode_e4m3", "sink_attn_decode_e4m3_f8pv", "sink_attn_selftest_wait")
+           "sink_attn_decode_e4m3", "sink_attn_decode_e4m3_f8pv", "sink_attn_selftest_wait",
+           "sink_attn_paged_plan", "sink_attn_paged_append", "sink_attn_paged_append_e4m3",
+           "sink_attn_paged_workspace_size", "sink_attn_paged_attn", "sink_attn_paged_attn_e4m3")
 
 
 class SinkAttnError(RuntimeError):
@@ -46,6 +48,19 @@ class DecodeDims(ctypes.Structure):
     _fields_ = [("batch", ctypes.c_int), ("new_tokens", ctypes.c_int), ("cache_capacity", ctypes.c_int),
                 ("max_seqlen", ctypes.c_int), ("num_q_heads", ctypes.c_int), ("num_kv_heads", ctypes.c_int),
                 ("head_dim", ctypes.c_int)]
+
+
+class PlanDims(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int), ("max_tokens", ctypes.c_int), ("max_pages", ctypes.c_int),
+                ("page_size", ctypes.c_int), ("num_pages", ctypes.c_int)]
+
+
+class PagedDims(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int), ("total_tokens", ctypes.c_int), ("max_new", ctypes.c_int),
+                ("num_q_heads", ctypes.c_int), ("num_kv_heads", ctypes.c_int), ("head_dim", ctypes.c_int),
+                ("page_size", ctypes.c_int), ("num_pages", ctypes.c_int), ("max_pages", ctypes.c_int),
+                ("page_stride", ctypes.c_longlong), ("token_stride", ctypes.c_longlong),
+                ("head_stride", ctypes.c_longlong), ("q_stride", ctypes.c_longlong)]
 
 
 def lib_path() -> str:
@@ -101,6 +116,21 @@ def load():
         L.sink_attn_decode_launches.restype = I
         L.sink_attn_selftest_wait.argtypes = [ctypes.c_ulonglong, P, P]
         L.sink_attn_selftest_wait.restype = I
+        PD = ctypes.POINTER(PagedDims)
+        LL = ctypes.c_longlong
+        L.sink_attn_paged_plan.argtypes = [ctypes.POINTER(PlanDims), P, P, P, P, P, P, I, P, P, P, P, P, P]
+        L.sink_attn_paged_plan.restype = I
+        L.sink_attn_paged_append.argtypes = [PD, P, P, LL, LL, P, P, P, P]
+        L.sink_attn_paged_append.restype = I
+        L.sink_attn_paged_append_e4m3.argtypes = [PD, P, P, LL, LL, P, P, P, P, P, P]
+        L.sink_attn_paged_append_e4m3.restype = I
+        L.sink_attn_paged_workspace_size.argtypes = [PD]
+        L.sink_attn_paged_workspace_size.restype = ctypes.c_size_t
+        L.sink_attn_paged_attn.argtypes = [PD, P, P, P, P, P, P, P, I, ctypes.c_float, P, P, P, ctypes.c_size_t, P]
+        L.sink_attn_paged_attn.restype = I
+        L.sink_attn_paged_attn_e4m3.argtypes = [PD, P, P, P, P, P, P, P, P, P, I, ctypes.c_float, P, P, P,
+                                                ctypes.c_size_t, P]
+        L.sink_attn_paged_attn_e4m3.restype = I
         _lib = L
     return _lib
 
@@ -308,6 +338,184 @@ def decode_e4m3(q, k_new, v_new, k_cache, v_cache, cache_seqlens, k_scale, v_sca
 def decode_e4m3_f8pv(*args, **kw):
     """sink_attn_decode_e4m3_f8pv (see decode_e4m3)."""
     return decode_e4m3(*args, f8pv=True, **kw)
+
+
+def _check(t, name, dtype, shape, device, strides=False):
+    """Refuses a tensor of another type, shape (None: any length) or device
+    than a paged call takes, or, unless strides are the call's to give, one
+    that is not contiguous."""
+    if not t.is_cuda:
+        raise ValueError(f"{name}: expected a CUDA tensor, got one on {t.device}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the call's other tensors are on {device}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
+        raise ValueError(f"{name}: expected shape {shape}, got {tuple(t.shape)}")
+    if not strides and not t.is_contiguous():
+        raise ValueError(f"{name} is not contiguous")
+
+
+def _on(device, stream):
+    """The stream of a paged call.  Work goes to the given stream, or to the
+    current one of the tensors' device, with that device current."""
+    if stream is None:
+        return torch.cuda.current_stream(device)
+    if stream.device != device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors are on {device}")
+    return stream
+
+
+def _paged_cache(k_cache, v_cache, k_scale, v_scale):
+    """Checks a paged cache; returns (codes, num_pages, page_size, Hkv)."""
+    codes = k_cache.dtype in (torch.uint8, torch.float8_e4m3fn)
+    if not codes and k_cache.dtype != torch.bfloat16:
+        raise ValueError(f"k_cache: expected bfloat16, float8_e4m3fn or uint8 codes, got {k_cache.dtype}")
+    _check(k_cache, "k_cache", k_cache.dtype, (None, None, None, 64), k_cache.device, strides=True)
+    _check(v_cache, "v_cache", k_cache.dtype, tuple(k_cache.shape), k_cache.device, strides=True)
+    if k_cache.stride() != v_cache.stride() or k_cache.stride(3) != 1:
+        raise ValueError("k_cache and v_cache need the same strides, with contiguous rows")
+    pages, page, hkv, _ = k_cache.shape
+    if codes:
+        if k_scale is None or v_scale is None:
+            raise ValueError("an e4m3 cache needs k_scale and v_scale")
+        _check(k_scale, "k_scale", torch.float32, (hkv,), k_cache.device)
+        _check(v_scale, "v_scale", torch.float32, (hkv,), k_cache.device)
+    elif k_scale is not None or v_scale is not None:
+        raise ValueError("a bf16 cache takes no scales")
+    return codes, pages, page, hkv
+
+
+def paged_plan(cached_lens, new_lens, block_table, free_pages, pool, page_size, max_tokens, window=0, first_page=None,
+               *, cu_seqlens=None, kv_lens=None, slot_map=None, pool_out=None, first_page_out=None, stream=None):
+    """sink_attn_paged_plan: one step's pages and slots from the requests'
+    lengths.  cached_lens, new_lens [B] (new_lens < 0: the request has ended),
+    block_table [B, max_pages] and free_pages [num_pages] (both updated in
+    place), pool [2] = (head, count) of the ring of free pages, first_page [B]
+    or None; all int32 CUDA.  Returns (cu_seqlens [B + 1], kv_lens [B],
+    slot_map [max_tokens], pool_out [2], first_page_out [B] or None).
+    kv_lens, pool_out and first_page_out may be given as cached_lens, pool and
+    first_page, which updates those in place."""
+    dev, i32 = cached_lens.device, torch.int32
+    B = cached_lens.numel()
+    _check(cached_lens, "cached_lens", i32, (B,), dev)
+    _check(new_lens, "new_lens", i32, (B,), dev)
+    _check(block_table, "block_table", i32, (B, None), dev)
+    _check(free_pages, "free_pages", i32, (None,), dev)
+    _check(pool, "pool", i32, (2,), dev)
+    if first_page is not None:
+        _check(first_page, "first_page", i32, (B,), dev)
+    elif window > 0 or first_page_out is not None:
+        raise ValueError("giving back a window's pages needs first_page")
+    s = _on(dev, stream)
+    with torch.cuda.stream(s):
+        def made(t, name, n):
+            if t is None:
+                return torch.empty((n,), dtype=i32, device=dev)
+            _check(t, name, i32, (n,), dev)
+            return t
+        cu_seqlens = made(cu_seqlens, "cu_seqlens", B + 1)
+        kv_lens = made(kv_lens, "kv_lens", B)
+        slot_map = made(slot_map, "slot_map", max_tokens)
+        pool_out = made(pool_out, "pool_out", 2)
+        if first_page is not None:
+            first_page_out = made(first_page_out, "first_page_out", B)
+        if B == 0:
+            cu_seqlens.zero_()
+            slot_map.fill_(-1)
+            pool_out.copy_(pool)
+            return cu_seqlens, kv_lens, slot_map, pool_out, first_page_out
+        dims = PlanDims(B, int(max_tokens), block_table.shape[1], int(page_size), free_pages.numel())
+        st = load().sink_attn_paged_plan(
+            ctypes.byref(dims), _ptr(cached_lens), _ptr(new_lens), _ptr(block_table), _ptr(free_pages), _ptr(pool),
+            _ptr(first_page), int(window), _ptr(cu_seqlens), _ptr(kv_lens), _ptr(slot_map), _ptr(pool_out),
+            _ptr(first_page_out), ctypes.c_void_p(s.cuda_stream))
+    if st != 0:
+        raise SinkAttnError(st, "sink_attn_paged_plan")
+    return cu_seqlens, kv_lens, slot_map, pool_out, first_page_out
+
+
+def paged_append(k_new, v_new, slot_map, k_cache, v_cache, k_scale=None, v_scale=None, *, stream=None):
+    """sink_attn_paged_append (bf16 cache) or sink_attn_paged_append_e4m3 (a
+    cache of e4m3 codes, with k_scale / v_scale fp32 [Hkv]).  k_new / v_new
+    [T, Hkv, D] bf16, at any token stride; slot_map int32 [T], negative slots
+    are skipped; k_cache / v_cache [num_pages, page_size, Hkv, D], updated in
+    place.  Returns (k_cache, v_cache)."""
+    codes, pages, page, hkv = _paged_cache(k_cache, v_cache, k_scale, v_scale)
+    dev, T = k_cache.device, k_new.shape[0]
+    _check(k_new, "k_new", torch.bfloat16, (T, hkv, 64), dev, strides=True)
+    _check(v_new, "v_new", torch.bfloat16, (T, hkv, 64), dev, strides=True)
+    _check(slot_map, "slot_map", torch.int32, (T,), dev)
+    for name, t in (("k_new", k_new), ("v_new", v_new)):
+        if t.stride(2) != 1 or (hkv > 1 and t.stride(1) != 64):
+            raise ValueError(f"{name}: the heads of a token are not contiguous")
+    s = _on(dev, stream)
+    st_ = k_cache.stride()
+    dims = PagedDims(0, T, 0, 0, hkv, 64, page, pages, 0, st_[0], st_[1], st_[2], 0)
+    L = load()
+    with torch.cuda.stream(s):
+        if codes:
+            st = L.sink_attn_paged_append_e4m3(ctypes.byref(dims), _ptr(k_new), _ptr(v_new), k_new.stride(0),
+                                               v_new.stride(0), _ptr(slot_map), _ptr(k_cache), _ptr(v_cache),
+                                               _ptr(k_scale), _ptr(v_scale), ctypes.c_void_p(s.cuda_stream))
+        else:
+            st = L.sink_attn_paged_append(ctypes.byref(dims), _ptr(k_new), _ptr(v_new), k_new.stride(0),
+                                          v_new.stride(0), _ptr(slot_map), _ptr(k_cache), _ptr(v_cache),
+                                          ctypes.c_void_p(s.cuda_stream))
+    if st != 0:
+        raise SinkAttnError(st, "sink_attn_paged_append_e4m3" if codes else "sink_attn_paged_append")
+    return k_cache, v_cache
+
+
+def paged_attn(q, k_cache, v_cache, block_table, cu_seqlens, kv_lens, sinks, window=0, scale=None, *, max_new=None,
+               k_scale=None, v_scale=None, out=None, lse=None, workspace=None, stream=None):
+    """sink_attn_paged_attn (bf16 cache) or sink_attn_paged_attn_e4m3 (a cache
+    of e4m3 codes): the packed new tokens q [T, Hq, D] bf16 (any token stride)
+    attend over the pages of k_cache / v_cache [num_pages, page_size, Hkv, D]
+    that block_table int32 [B, max_pages] names.  cu_seqlens int32 [B + 1],
+    kv_lens int32 [B] (tokens after the step, the new ones included), sinks
+    [Hq] fp32.  max_new bounds the new tokens of one request (default T).
+    Returns (out [T, Hq, D], lse [Hq, T]); rows behind cu_seqlens[B] are left
+    as they were."""
+    codes, pages, page, hkv = _paged_cache(k_cache, v_cache, k_scale, v_scale)
+    dev = k_cache.device
+    T, Hq, D = q.shape
+    B = kv_lens.numel()
+    _check(q, "q", torch.bfloat16, (T, Hq, 64), dev, strides=True)
+    if q.stride(2) != 1 or (Hq > 1 and q.stride(1) != 64):
+        raise ValueError("q: the heads of a token are not contiguous")
+    _check(block_table, "block_table", torch.int32, (B, None), dev)
+    _check(cu_seqlens, "cu_seqlens", torch.int32, (B + 1,), dev)
+    _check(kv_lens, "kv_lens", torch.int32, (B,), dev)
+    _check(sinks, "sinks", torch.float32, (Hq,), dev)
+    s = _on(dev, stream)
+    st_ = k_cache.stride()
+    dims = PagedDims(B, T, int(max(T, 1) if max_new is None else max_new), Hq, hkv, 64, page, pages,
+                     block_table.shape[1], st_[0], st_[1], st_[2], q.stride(0))
+    L = load()
+    with torch.cuda.stream(s):
+        if out is None:
+            out = torch.empty((T, Hq, 64), dtype=torch.bfloat16, device=dev)
+        else:
+            _check(out, "out", torch.bfloat16, (T, Hq, 64), dev)
+        if lse is None:
+            lse = torch.empty((Hq, T), dtype=torch.float32, device=dev)
+        else:
+            _check(lse, "lse", torch.float32, (Hq, T), dev)
+        if workspace is None:
+            need = int(L.sink_attn_paged_workspace_size(ctypes.byref(dims)))
+            workspace = torch.empty((max(need, 1),), dtype=torch.uint8, device=dev)
+        args = (ctypes.byref(dims), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_table), _ptr(cu_seqlens),
+                _ptr(kv_lens))
+        tail = (_ptr(sinks), int(window), float(D ** -0.5 if scale is None else scale), _ptr(out), _ptr(lse),
+                _ptr(workspace), ctypes.c_size_t(workspace.numel()), ctypes.c_void_p(s.cuda_stream))
+        if codes:
+            st = L.sink_attn_paged_attn_e4m3(*args, _ptr(k_scale), _ptr(v_scale), *tail)
+        else:
+            st = L.sink_attn_paged_attn(*args, *tail)
+    if st != 0:
+        raise SinkAttnError(st, "sink_attn_paged_attn_e4m3" if codes else "sink_attn_paged_attn")
+    return out, lse
 
 
 def device_error(stream=None) -> int:
