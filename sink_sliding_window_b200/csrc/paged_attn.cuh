@@ -1,22 +1,22 @@
-// Attention of a step's new tokens over a paged cache, plainly: one thread per
-// (token, query head) row, which walks its visible keys with a running maximum
-// and sum.
+// What the paged attention kernels share: a call's parameters and the rows and
+// keys of one request.
 #pragma once
 #include "decode_kernel.cuh"
 
 namespace sa {
 
+constexpr int kPagedMaxBatch = 4096;  // a call's request table is kept in shared memory
+
 struct PagedParams {
   int batch, T, Hq, Hkv, G;
   int max_new;
   int page_log2, num_pages, max_pages;
+  int box_log2;      // tokens of one TMA box of the few-rows kernel
+  int few;           // a request of at most this many new tokens goes to the few-rows kernel
   int window;        // 0: full causal
   float scale_log2;  // scale * log2(e)
   long long q_stride;
-  long long page_stride, token_stride, head_stride;
   const __nv_bfloat16* q;
-  const void* k_cache;
-  const void* v_cache;
   const float* k_scale;
   const float* v_scale;
   const int* table;
@@ -25,99 +25,59 @@ struct PagedParams {
   const float* sinks;
   __nv_bfloat16* out;
   float* lse;
+  // Workspace of the few-rows kernel, per worker (a warp): two partial results
+  // (unnormalised O, reference max, sum) and which unit it completes.
+  float* part_o;     // [workers][2][kR][64]
+  float2* part_ml;   // [workers][2][kR] (m in log2 units, l)
+  int4* part_unit;   // [workers] (b or -1, g, first worker, 0)
 };
 
-template <bool kF8>
-__device__ __forceinline__ void paged_row(const void* cache, long long at, float* x) {
-  if constexpr (kF8) {
-    const uint4* s = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(cache) + at);
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const uint4 v = __ldg(s + c);
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        const uint32_t h2 = e4m3x2_to_f16x2(w[u / 2] >> (16 * (u & 1)));
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h2));
-        x[16 * c + 2 * u] = f.x;
-        x[16 * c + 2 * u + 1] = f.y;
-      }
-    }
-  } else {
-    const uint4* s = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(cache) + at);
-#pragma unroll
-    for (int c = 0; c < 8; ++c) {
-      const uint4 v = __ldg(s + c);
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        x[8 * c + 2 * u] = __uint_as_float(w[u] << 16);
-        x[8 * c + 2 * u + 1] = __uint_as_float(w[u] & 0xFFFF0000u);
-      }
-    }
-  }
+// One request's rows and keys.  Lengths that do not fit the call's sizes are
+// cut to them (and reported by paged_check), so that no index leaves a tensor.
+struct PagedRequest {
+  int t0, n;   // first row of q and new tokens
+  int len;     // tokens after the step
+  int lo;      // first key that any of its rows sees; the last one is len - 1
+};
+
+__device__ __forceinline__ PagedRequest paged_request(const PagedParams& p, int b) {
+  PagedRequest r;
+  r.t0 = min(max(__ldg(p.cu + b), 0), p.T);
+  r.n = min(max(__ldg(p.cu + b + 1), r.t0), p.T) - r.t0;
+  r.len = min(max(__ldg(p.kv_lens + b), 0), p.max_pages << p.page_log2);
+  r.lo = p.window > 0 ? max(0, r.len - r.n - p.window + 1) : 0;
+  return r;
 }
 
-template <bool kF8>
-__global__ void __launch_bounds__(128) sink_attn_paged_kernel(const PagedParams p) {
-  const long long r = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
-  const int g = blockIdx.y;
-  const int t = static_cast<int>(r / p.G);
-  if (r == 0 && __ldg(p.cu + p.batch) > p.T) atomicCAS(&g_device_error, 0, static_cast<int>(kDevErrPagedRows));
-  if (t >= p.T || t >= __ldg(p.cu + p.batch)) return;
-  const int h = g * p.G + static_cast<int>(r % p.G);
-  int lo = 0, hi = p.batch - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (__ldg(p.cu + mid) <= t) lo = mid; else hi = mid - 1;
-  }
-  const int b = lo;
-  if (__ldg(p.cu + b + 1) - __ldg(p.cu + b) > p.max_new) atomicCAS(&g_device_error, 0, static_cast<int>(kDevErrPagedRows));
-  const int len = min(max(__ldg(p.kv_lens + b), 0), p.max_pages << p.page_log2);
-  const int i = len - (__ldg(p.cu + b + 1) - t);
-  float q[kHeadDim], o[kHeadDim];
-  paged_row<false>(p.q, t * p.q_stride + h * kHeadDim, q);
-#pragma unroll
-  for (int d = 0; d < kHeadDim; ++d) o[d] = 0.f;
-  const float sl2 = kF8 ? p.scale_log2 * __ldg(p.k_scale + g) : p.scale_log2;
-  float m = __ldg(p.sinks + h) * kLog2e;
-  // The sum is kept in two levels, 64 keys and all of them: thousands of small
-  // weights added one by one to a sum near 1 would lose their low bits.
-  float l = m == -INFINITY ? 0.f : 1.f, l64 = 0.f;
-  for (int j = p.window > 0 ? max(0, i - p.window + 1) : 0; j <= i; ++j) {
-    const int page = __ldg(p.table + static_cast<long long>(b) * p.max_pages + (j >> p.page_log2));
-    if (page < 0 || page >= p.num_pages) {
-      atomicCAS(&g_device_error, 0, static_cast<int>(kDevErrBadPage));
-      continue;
-    }
-    const long long at = page * p.page_stride + (j & ((1 << p.page_log2) - 1)) * p.token_stride + g * p.head_stride;
-    float x[kHeadDim];
-    paged_row<kF8>(p.k_cache, at, x);
-    float s = 0.f;
-#pragma unroll
-    for (int d = 0; d < kHeadDim; ++d) s = fmaf(q[d], x[d], s);
-    s *= sl2;
-    if (s > m) {
-      const float f = exp2f(m - s);
-      l *= f;
-      l64 *= f;
-#pragma unroll
-      for (int d = 0; d < kHeadDim; ++d) o[d] *= f;
-      m = s;
-    }
-    const float w = m == -INFINITY ? 0.f : exp2f(s - m);
-    l64 += w;
-    if ((j & 63) == 63) l += l64, l64 = 0.f;
-    paged_row<kF8>(p.v_cache, at, x);
-#pragma unroll
-    for (int d = 0; d < kHeadDim; ++d) o[d] = fmaf(w, x[d], o[d]);
-  }
-  l += l64;
-  const float f = l > 0.f ? (kF8 ? __ldg(p.v_scale + g) : 1.f) / l : 0.f;
-  __nv_bfloat16* dst = p.out + (static_cast<long long>(t) * p.Hq + h) * kHeadDim;
-#pragma unroll
-  for (int d = 0; d < kHeadDim; ++d) dst[d] = __float2bfloat16_rn(o[d] * f);
-  p.lse[static_cast<long long>(h) * p.T + t] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+// Reports a request whose lengths do not fit.
+__device__ __forceinline__ void paged_check(const PagedParams& p, int b) {
+  const int c0 = __ldg(p.cu + b), c1 = __ldg(p.cu + b + 1), len = __ldg(p.kv_lens + b);
+  if (c0 < 0 || c1 < c0 || c1 > p.T || c1 - c0 > p.max_new || len < 0 || len > (p.max_pages << p.page_log2))
+    atomicCAS(&g_device_error, 0, static_cast<int>(kDevErrPagedRows));
 }
+
+// The page that holds key j of request b, or num_pages (which a TMA load reads
+// as zeros) when the table's entry lies outside the pool.
+__device__ __forceinline__ int paged_page(const PagedParams& p, int b, int j) {
+  const int page = __ldg(p.table + static_cast<long long>(b) * p.max_pages + (j >> p.page_log2));
+  if (page >= 0 && page < p.num_pages) return page;
+  atomicCAS(&g_device_error, 0, static_cast<int>(kDevErrBadPage));
+  return p.num_pages;
+}
+
+// 4-D tiled load global -> shared (see tma_load_3d).
+__device__ __forceinline__ void tma_load_4d(void* smem_dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z,
+                                            int w) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_u32(smem_dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "r"(w)
+      : "memory");
+}
+
+// Programmatic dependent launch: lets the next kernel of the stream start, and
+// waits until the kernels before this one have completed.
+__device__ __forceinline__ void pdl_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 }  // namespace sa

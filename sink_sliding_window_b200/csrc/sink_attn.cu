@@ -21,6 +21,8 @@
 #include "paged_plan.cuh"
 #include "paged_append.cuh"
 #include "paged_attn.cuh"
+#include "paged_rows.cuh"
+#include "paged_long.cuh"
 
 namespace sa {
 namespace {
@@ -646,12 +648,117 @@ sink_attn_status check_paged_attn(const sink_attn_paged_dims* d, bool codes) {
   if (d->batch < 0 || d->max_new <= 0 || d->max_pages <= 0 || d->num_q_heads <= 0 || d->q_stride < 0)
     return SINK_ATTN_ERR_SHAPE;
   if (d->num_q_heads % d->num_kv_heads != 0) return SINK_ATTN_ERR_SHAPE;
-  if (d->num_q_heads / d->num_kv_heads > kBlockM) return SINK_ATTN_ERR_UNSUPPORTED;
-  // Positions are 32-bit, with room for a tile behind the last one.
-  if (static_cast<int64_t>(d->max_pages) * d->page_size > (int64_t(1) << 30) || d->batch > (1 << 24))
-    return SINK_ATTN_ERR_UNSUPPORTED;
+  if (d->num_q_heads / d->num_kv_heads > kBlockM || d->batch > kPagedMaxBatch) return SINK_ATTN_ERR_UNSUPPORTED;
+  // Positions are 32-bit, with room for a tile behind the last one; so are the
+  // blocks of keys of all requests, and a worker's share of them.
+  const int64_t tokens = static_cast<int64_t>(d->max_pages) * d->page_size;
+  if (tokens > (int64_t(1) << 30) || tokens * std::max(d->batch, 1) > (int64_t(1) << 35)) return SINK_ATTN_ERR_UNSUPPORTED;
   if (d->q_stride % 8) return SINK_ATTN_ERR_ALIGN;
   return SINK_ATTN_OK;
+}
+
+// Which kernels a call's requests go to.  A request of at most `few` new
+// tokens is the few-rows kernel's (kR rows: 8, 16 or 32, the smallest that
+// holds the call's requests if one does, else one token of a group).
+struct PagedSplit {
+  int kR, few;
+  bool rows, chunks;
+};
+
+PagedSplit split_paged(const sink_attn_paged_dims* d) {
+  PagedSplit s;
+  const int G = d->num_q_heads / d->num_kv_heads;
+  const int64_t need = static_cast<int64_t>(std::min(d->max_new, d->total_tokens)) * G;
+  const int64_t fit = need <= kRowsMaxRows ? need : G;
+  s.kR = fit <= 8 ? 8 : fit <= 16 ? 16 : 32;
+  s.few = s.kR / G;
+  s.rows = s.few > 0;
+  s.chunks = need > static_cast<int64_t>(s.few) * G;
+  return s;
+}
+
+constexpr int kPagedCtas = 148;  // one CTA per SM of a B200
+constexpr int kPagedWorkers = kPagedCtas * kRowsWarps;
+
+// Workspace of a call (bytes): the pieces of cut units.
+struct PagedWorkspace {
+  size_t unit, ml, o, total;
+};
+
+PagedWorkspace paged_workspace(const PagedSplit& s) {
+  PagedWorkspace w = {0, 0, 0, 256};
+  if (s.rows) {
+    w.ml = round256(kPagedWorkers * sizeof(int4));
+    w.o = w.ml + round256(kPagedWorkers * 2 * static_cast<size_t>(s.kR) * sizeof(float2));
+    w.total = w.o + kPagedWorkers * 2 * static_cast<size_t>(s.kR) * kHeadDim * sizeof(float);
+  }
+  return w;
+}
+
+// 4-D view [page][token][head][64] of a paged cache with a box of `tokens`
+// tokens of one head: 128-byte rows (bf16) under the 128-byte swizzle, or
+// 64-byte rows (codes) under the 64-byte swizzle.
+bool make_map_paged(CUtensorMap* map, const void* base, const sink_attn_paged_dims* d, bool codes, int tokens) {
+  EncodeTiledFn enc = get_encode_tiled();
+  if (!enc) return false;
+  const cuuint64_t size = codes ? 1 : 2;
+  cuuint64_t dims[4] = {kHeadDim, static_cast<cuuint64_t>(d->num_kv_heads), static_cast<cuuint64_t>(d->page_size),
+                        static_cast<cuuint64_t>(d->num_pages)};
+  cuuint64_t strides[3] = {static_cast<cuuint64_t>(d->head_stride) * size,
+                           static_cast<cuuint64_t>(d->token_stride) * size,
+                           static_cast<cuuint64_t>(d->page_stride) * size};
+  // The stride of a dimension of one element is never used, and may be anything.
+  for (int i = 0; i < 3; ++i)
+    if (dims[i + 1] == 1) strides[i] = kHeadDim * size;
+  cuuint32_t box[4] = {kHeadDim, 1, static_cast<cuuint32_t>(tokens), 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  return enc(map, codes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base),
+             dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             codes ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The longest unit of a call, in blocks, is short enough that no cut is left
+// inside one (see RowsAxis::cut): nothing to join.
+template <bool kF8>
+bool rows_never_cut(const PagedParams& p) {
+  const int64_t keys = p.window > 0 ? static_cast<int64_t>(p.window) + p.few - 1 : int64_t(p.max_pages) << p.page_log2;
+  const int64_t lead = p.window > 0 ? (1 << p.box_log2) - 1 : 0;
+  return (keys + lead + kRowsKeys<kF8> - 1) / kRowsKeys<kF8> <= 2 * kRowsSnap<kF8> + 1;
+}
+
+template <bool kF8, int kR>
+bool launch_rows(PagedParams& p, const sink_attn_paged_dims* d, const void* k_cache, const void* v_cache,
+                 cudaStream_t st) {
+  const int box = std::min(d->page_size, kRowsKeys<kF8>);
+  p.box_log2 = ilog2_exact(box);
+  CUtensorMap tm_k, tm_v;
+  if (!make_map_paged(&tm_k, k_cache, d, kF8, box) || !make_map_paged(&tm_v, v_cache, d, kF8, box)) return false;
+  static SmemAttrOnce smem_set;
+  if (!smem_set.ensure(sink_attn_paged_rows_kernel<kF8, kR>, rows_smem_bytes(kPagedMaxBatch))) return false;
+  const bool join = !rows_never_cut<kF8>(p);
+  if (!join) p.part_unit = nullptr;
+  sink_attn_paged_rows_kernel<kF8, kR><<<kPagedCtas, kRowsThreads, rows_smem_bytes(p.batch), st>>>(tm_k, tm_v, p);
+  if (cudaPeekAtLastError() != cudaSuccess) return false;
+  if (!join) return true;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(kPagedWorkers, 1, 1);
+  cfg.blockDim = dim3(256, 1, 1);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, sink_attn_paged_join_kernel<kR>, p) == cudaSuccess;
+}
+
+template <bool kF8>
+bool launch_rows(int kR, PagedParams& p, const sink_attn_paged_dims* d, const void* k_cache, const void* v_cache,
+                 cudaStream_t st) {
+  return kR == 8    ? launch_rows<kF8, 8>(p, d, k_cache, v_cache, st)
+         : kR == 16 ? launch_rows<kF8, 16>(p, d, k_cache, v_cache, st)
+                    : launch_rows<kF8, 32>(p, d, k_cache, v_cache, st);
 }
 
 sink_attn_status paged_attn_impl(const sink_attn_paged_dims* d, const void* q, const void* k_cache,
@@ -670,7 +777,9 @@ sink_attn_status paged_attn_impl(const sink_attn_paged_dims* d, const void* q, c
       !aligned4(cu_seqlens) || !aligned4(kv_lens) || !aligned4(sinks) || !aligned4(lse) || !aligned4(k_scale) ||
       !aligned4(v_scale))
     return SINK_ATTN_ERR_ALIGN;
-  if (workspace_bytes < sink_attn_paged_workspace_size(d) || !workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u))
+  const PagedSplit split = split_paged(d);
+  const PagedWorkspace ws = paged_workspace(split);
+  if (workspace_bytes < ws.total || !workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u))
     return SINK_ATTN_ERR_WORKSPACE;
   PagedParams p;
   p.batch = d->batch;
@@ -682,15 +791,12 @@ sink_attn_status paged_attn_impl(const sink_attn_paged_dims* d, const void* q, c
   p.page_log2 = ilog2_exact(d->page_size);
   p.num_pages = d->num_pages;
   p.max_pages = d->max_pages;
+  p.box_log2 = 0;
+  p.few = split.few;
   p.window = window > 0 ? window : 0;
   p.scale_log2 = scale * kLog2e;
   p.q_stride = d->q_stride;
-  p.page_stride = d->page_stride;
-  p.token_stride = d->token_stride;
-  p.head_stride = d->head_stride;
   p.q = static_cast<const __nv_bfloat16*>(q);
-  p.k_cache = k_cache;
-  p.v_cache = v_cache;
   p.k_scale = k_scale;
   p.v_scale = v_scale;
   p.table = block_table;
@@ -699,12 +805,21 @@ sink_attn_status paged_attn_impl(const sink_attn_paged_dims* d, const void* q, c
   p.sinks = sinks;
   p.out = static_cast<__nv_bfloat16*>(out);
   p.lse = lse;
-  const long long rows = static_cast<long long>(p.T) * p.G;
-  if ((rows + 127) / 128 > 0x7fffffff || p.Hkv > 65535) return SINK_ATTN_ERR_UNSUPPORTED;
-  const dim3 grid(static_cast<unsigned>((rows + 127) / 128), static_cast<unsigned>(p.Hkv));
+  uint8_t* base = static_cast<uint8_t*>(workspace);
+  p.part_unit = reinterpret_cast<int4*>(base + ws.unit);
+  p.part_ml = reinterpret_cast<float2*>(base + ws.ml);
+  p.part_o = reinterpret_cast<float*>(base + ws.o);
   cudaStream_t st_ = static_cast<cudaStream_t>(stream);
-  if (codes) sink_attn_paged_kernel<true><<<grid, 128, 0, st_>>>(p);
-  else sink_attn_paged_kernel<false><<<grid, 128, 0, st_>>>(p);
+  if (split.rows && !(codes ? launch_rows<true>(split.kR, p, d, k_cache, v_cache, st_)
+                            : launch_rows<false>(split.kR, p, d, k_cache, v_cache, st_)))
+    return SINK_ATTN_ERR_CUDA;
+  if (split.chunks) {
+    const long long rows = static_cast<long long>(p.T) * p.G;
+    if ((rows + 127) / 128 > 0x7fffffff || p.Hkv > 65535) return SINK_ATTN_ERR_UNSUPPORTED;
+    const dim3 grid(static_cast<unsigned>((rows + 127) / 128), static_cast<unsigned>(p.Hkv));
+    if (codes) sink_attn_paged_kernel<true><<<grid, 128, 0, st_>>>(p, k_cache, v_cache, d->page_stride, d->token_stride, d->head_stride);
+    else sink_attn_paged_kernel<false><<<grid, 128, 0, st_>>>(p, k_cache, v_cache, d->page_stride, d->token_stride, d->head_stride);
+  }
   return cudaPeekAtLastError() == cudaSuccess ? SINK_ATTN_OK : SINK_ATTN_ERR_CUDA;
 }
 
@@ -791,7 +906,7 @@ sink_attn_status sink_attn_paged_append_e4m3(const sink_attn_paged_dims* d, cons
 }
 
 size_t sink_attn_paged_workspace_size(const sink_attn_paged_dims* d) {
-  return check_paged_attn(d, false) == SINK_ATTN_OK ? 256 : 0;
+  return check_paged_attn(d, false) == SINK_ATTN_OK ? paged_workspace(split_paged(d)).total : 0;
 }
 
 sink_attn_status sink_attn_paged_attn(const sink_attn_paged_dims* d, const void* q, const void* k_cache,
