@@ -25,11 +25,13 @@ struct PagedParams {
   const float* sinks;
   __nv_bfloat16* out;
   float* lse;
-  // Workspace of the few-rows kernel, per worker (a warp): two partial results
-  // (unnormalised O, reference max, sum) and which unit it completes.
-  float* part_o;     // [workers][2][kR][64]
-  float2* part_ml;   // [workers][2][kR] (m in log2 units, l)
-  int4* part_unit;   // [workers] (b or -1, g, first worker, 0)
+  // The few-rows kernel: key/value heads in chunks, and its workspace, per
+  // worker two partial results for each head of a chunk (unnormalised O,
+  // reference max, sum) and which request it completes.
+  int chunks, per_chunk;
+  float* part_o;     // [workers][2][per_chunk][kR][64]
+  float2* part_ml;   // [workers][2][per_chunk][kR] (m in log2 units, l)
+  int4* part_unit;   // [workers] (b or -1, chunk, first worker, 0)
 };
 
 // One request's rows and keys.  Lengths that do not fit the call's sizes are
@@ -56,11 +58,15 @@ __device__ __forceinline__ void paged_check(const PagedParams& p, int b) {
     atomicCAS(&g_device_error, 0, static_cast<int>(kDevErrPagedRows));
 }
 
-// The page that holds key j of request b, or num_pages (which a TMA load reads
-// as zeros) when the table's entry lies outside the pool.
-__device__ __forceinline__ int paged_page(const PagedParams& p, int b, int j) {
-  const int page = __ldg(p.table + static_cast<long long>(b) * p.max_pages + (j >> p.page_log2));
-  if (page >= 0 && page < p.num_pages) return page;
+// The table's entry for the page that holds key j of request b.
+__device__ __forceinline__ int paged_entry(const PagedParams& p, int b, int j) {
+  return __ldg(p.table + static_cast<long long>(b) * p.max_pages + (j >> p.page_log2));
+}
+
+// A table entry as a page: num_pages, which a TMA load reads as zeros, when it
+// lies outside the pool.
+__device__ __forceinline__ int paged_page(const PagedParams& p, int entry) {
+  if (entry >= 0 && entry < p.num_pages) return entry;
   atomicCAS(&g_device_error, 0, static_cast<int>(kDevErrBadPage));
   return p.num_pages;
 }

@@ -1,14 +1,18 @@
 // Paged attention of requests with few query rows (single tokens above all):
 // the keys and values of a request cross HBM once, and that is what bounds it.
 //
-// A unit is one (request, key/value head); its n * G query rows (n new tokens,
-// G heads) fill one or two 16-row MMA tiles, and its visible keys are cut into
-// blocks of kKeys keys.  The blocks of all units, in order, are one axis, of
-// which every warp of the grid takes an equal piece: no share depends on how
-// ragged the lengths are, and the host needs to know none of them.  A warp is a
-// worker of its own: it fetches its blocks with TMA into a ring of its own in
-// shared memory, kStages blocks ahead, and keeps running maximum, sum and O in
-// registers; workers meet nowhere.  The tiles come to the tensor cores through
+// A request's visible keys are cut into blocks of kKeys keys.  The blocks of
+// all requests, in order, are one axis, of which every worker takes an equal
+// piece: no share depends on how ragged the lengths are, and the host needs to
+// know none of them.  A worker is a group of warps, one for each of up to
+// eight key/value heads: the heads of a token lie side by side in most caches,
+// so that warps which read the same tokens at about the same time read whole
+// DRAM pages (with the heads one after another on the axis instead, the same
+// tokens crossed HBM 1.3 times, and 64 x 6-8k took 219 us for 142 us of
+// bytes).  The warps of a worker share nothing else: each fetches its blocks
+// with TMA into a ring of its own in shared memory, kStages blocks ahead, and
+// keeps running maximum, sum and O of its n * G query rows (n new tokens, G
+// heads; one or two 16-row MMA tiles) in registers.  The tiles come to the tensor cores through
 // mma.sync: with 8 or 16 rows the S and P of a block are a few registers, and
 // the trip through tensor memory that the 128-row instructions need costs more
 // than the multiplication (the decode kernel over linear caches makes that
@@ -17,8 +21,8 @@
 //   P = 2^(S sl2 - m)  m: running maximum of the row
 //   O = O 2^(m' - m) + P V
 // The accumulators of S hold what the first operand of PV wants, so P never
-// leaves the registers.  A unit that lies within one worker's piece is written
-// out by it; the pieces of a cut unit go to the workspace and are joined by
+// leaves the registers.  A request that lies within one worker's piece is
+// written out by it; the pieces of a cut one go to the workspace and are joined by
 // the combine kernel, which adds the sink once.  The running maximum starts at
 // -inf, not at the sink: a sink far above the logits would push every weight
 // below the range of fp16.
@@ -42,7 +46,7 @@ constexpr int kRowsStages = 3;
 constexpr int kRowsTile = 4096;  // bytes of a K or a V block: 32 bf16 keys or 64 e4m3 keys
 constexpr int kRowsRing = kRowsStages * 2 * kRowsTile;
 constexpr int kRowsMaxRows = 32;
-// A cut closer than this many blocks to a unit's end moves there: joining a
+// A cut closer than this many blocks to a request's end moves there: joining a
 // piece costs more than reading so few keys.
 template <bool kF8>
 constexpr int kRowsSnap = kF8 ? 1 : 2;
@@ -94,15 +98,16 @@ __device__ __forceinline__ int rows_blocks(const PagedParams& p, const PagedRequ
   return max(1, (r.len - rows_first<kF8>(p, r) + kRowsKeys<kF8> - 1) / kRowsKeys<kF8>);
 }
 
-// The axis of all blocks: request by request, within it head by head.
+// The axis of all blocks: request by request, and within it chunk by chunk of
+// its key/value heads (one chunk when there are at most kRowsWarps heads).
 struct RowsAxis {
-  const int* pre;  // blocks of one head before request b, [batch + 1]
-  int batch, Hkv;
+  const int* pre;  // blocks before request b (of one chunk), [batch + 1]
+  int batch, chunks;
   long long total;
   int workers;
 
   __device__ __forceinline__ int find(long long x) const {  // the request of block x < total
-    const int q = static_cast<int>(x / Hkv);
+    const int q = static_cast<int>(x / chunks);
     int lo = 0, hi = batch - 1;
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
@@ -117,7 +122,7 @@ struct RowsAxis {
     if (w >= workers || x >= total) return total;
     const int b = find(x);
     const int blocks = pre[b + 1] - pre[b];
-    const int off = static_cast<int>((x - static_cast<long long>(pre[b]) * Hkv) % blocks);
+    const int off = static_cast<int>((x - static_cast<long long>(pre[b]) * chunks) % blocks);
     if (off <= kSnap) return x - off;
     return blocks - off <= kSnap ? x + blocks - off : x;
   }
@@ -184,47 +189,52 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
   RowsAxis axis;
   axis.pre = pre;
   axis.batch = p.batch;
-  axis.Hkv = p.Hkv;
-  axis.total = static_cast<long long>(pre[p.batch]) * p.Hkv;
-  axis.workers = static_cast<int>(min(static_cast<long long>(gridDim.x) * kRowsWarps, axis.total));
-  const int worker = blockIdx.x * kRowsWarps + warp;
-  int4 unit = make_int4(-1, 0, 0, 0);  // the cut unit that this worker completes
-  if (worker >= axis.workers) {
-    if (p.part_unit && lane == 0) p.part_unit[worker] = unit;
-    return;
-  }
-  const long long x0 = axis.cut<kSnap>(worker);
-  const int count = static_cast<int>(axis.cut<kSnap>(worker + 1) - x0);
+  axis.chunks = p.chunks;
+  axis.total = static_cast<long long>(pre[p.batch]) * p.chunks;
+  const int per_cta = kRowsWarps / p.per_chunk;  // workers
+  axis.workers = static_cast<int>(min(static_cast<long long>(gridDim.x) * per_cta, axis.total));
+  const int hw = warp % p.per_chunk;  // this warp's head within its chunk
+  if (warp >= per_cta * p.per_chunk) return;
+  const int worker = blockIdx.x * per_cta + warp / p.per_chunk;
+  const bool reports = p.part_unit && hw == 0 && lane == 0;
+  int4 unit = make_int4(-1, 0, 0, 0);  // the cut request (and chunk) that this worker completes
+  const long long x0 = worker < axis.workers ? axis.cut<kSnap>(worker) : 0;
+  const int count = worker < axis.workers ? static_cast<int>(axis.cut<kSnap>(worker + 1) - x0) : 0;
   if (count == 0) {
-    if (p.part_unit && lane == 0) p.part_unit[worker] = unit;
+    if (reports) p.part_unit[worker] = unit;
     return;
   }
 
-  // The unit of the block that is computed next.
+  // The request and chunk of the block that is computed next.
   int b = axis.find(x0);
   int blocks = pre[b + 1] - pre[b];
-  int g = static_cast<int>((x0 - static_cast<long long>(pre[b]) * p.Hkv) / blocks);
-  int off = static_cast<int>((x0 - static_cast<long long>(pre[b]) * p.Hkv) % blocks);
+  int c = static_cast<int>((x0 - static_cast<long long>(pre[b]) * p.chunks) / blocks);
+  int off = static_cast<int>((x0 - static_cast<long long>(pre[b]) * p.chunks) % blocks);
   PagedRequest rq = paged_request(p, b);
   int first = rows_first<kF8>(p, rq);
 
-  // The unit of the block that is fetched next; its pages are looked up one
-  // block ahead of the copy.
-  int fb = b, fg = g, foff = off, fblocks = blocks, flen = rq.len, ffirst = first, fetched = 0;
+  // The same of the block that is fetched next; its pages are looked up one
+  // block ahead of the copy.  (The last chunk may have fewer heads: a warp
+  // without one reads the last head and writes nothing.)
+  auto head_of = [&](int chunk) { return min(chunk * p.per_chunk + hw, p.Hkv - 1); };
+  int fb = b, fc = c, foff = off, fblocks = blocks, flen = rq.len, ffirst = first, fetched = 0;
   uint8_t* ring = smem + warp * kRowsRing;
   uint64_t* full = ctl->full[warp];
   const int nbox = kKeys >> p.box_log2;
   const int page_mask = (1 << p.page_log2) - 1;
-  int next_page = p.num_pages, next_at = 0, next_g = 0;
+  int next_page = 0, next_at = 0, next_g = 0;
+  bool next_want = false;
   auto lookup = [&]() {
     const int j = ffirst + foff * kKeys + (lane << p.box_log2);
-    next_page = lane < nbox && j < flen ? paged_page(p, fb, j) : p.num_pages;
+    // Looked at by fetch(), so that the load is not waited for here.
+    next_want = lane < nbox && j < flen;
+    if (next_want) next_page = paged_entry(p, fb, j);
     next_at = j & page_mask;
-    next_g = fg;
+    next_g = head_of(fc);
     if (++foff == fblocks) {
       foff = 0;
-      if (++fg == p.Hkv) {
-        fg = 0;
+      if (++fc == p.chunks) {
+        fc = 0;
         if (fetched + 1 < count) {
           do ++fb; while (pre[fb + 1] == pre[fb]);
           fblocks = pre[fb + 1] - pre[fb];
@@ -241,8 +251,9 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
     __syncwarp();
     if (lane < nbox) {
       uint8_t* dst = ring + s * 2 * kRowsTile + (lane << p.box_log2) * kRow;
-      tma_load_4d(dst, &tm_k, &full[s], 0, next_g, next_at, next_page);
-      tma_load_4d(dst + kRowsTile, &tm_v, &full[s], 0, next_g, next_at, next_page);
+      const int page = next_want ? paged_page(p, next_page) : p.num_pages;
+      tma_load_4d(dst, &tm_k, &full[s], 0, next_g, next_at, page);
+      tma_load_4d(dst + kRowsTile, &tm_v, &full[s], 0, next_g, next_at, page);
     }
     if (fetched < count) lookup();
   };
@@ -253,7 +264,8 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
   uint32_t q[kMT][4][4];
   float o[kMT][8][4], m[kMT][2], l[kMT][2];
   int key_lo[kMT][2], key_hi[kMT][2];  // keys that this thread's rows see
-  bool seg_begin = true, whole = false;
+  bool seg_begin = true, whole = false, real = true;
+  int g = 0;
   float sl2 = 0.f;
   bool ok = true;
   int done = 0;
@@ -262,6 +274,8 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
     if (seg_begin) {
       seg_begin = false;
       whole = off == 0;
+      g = head_of(c);
+      real = c * p.per_chunk + hw < p.Hkv;
       sl2 = kF8 ? p.scale_log2 * __ldg(p.k_scale + g) : p.scale_log2;
 #pragma unroll
       for (int mt = 0; mt < kMT; ++mt) {
@@ -333,10 +347,10 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
         for (int mt = 0; mt < kMT; ++mt)
 #pragma unroll
           for (int u = 0; u < 4; ++u) x[mt][nt][u] = 0.f;
-        const int r = 32 * part + 8 * nt + (lane & 7), c = lane >> 3;
+        const int r = 32 * part + 8 * nt + (lane & 7), ch = lane >> 3;
         if constexpr (kF8) {
           uint32_t k[4];
-          ldsm4(sk + r * kRow + ((c ^ ((r >> 1) & 3)) << 4), k);
+          ldsm4(sk + r * kRow + ((ch ^ ((r >> 1) & 3)) << 4), k);
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
 #pragma unroll
@@ -344,8 +358,8 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
               mma_16816<true>(x[mt][nt], q[mt][kk], e4m3x2_to_f16x2(k[kk]), e4m3x2_to_f16x2(k[kk] >> 16));
         } else {
           uint32_t k[8];
-          ldsm4(sk + r * kRow + ((c ^ (r & 7)) << 4), k);
-          ldsm4(sk + r * kRow + (((c + 4) ^ (r & 7)) << 4), k + 4);
+          ldsm4(sk + r * kRow + ((ch ^ (r & 7)) << 4), k);
+          ldsm4(sk + r * kRow + (((ch + 4) ^ (r & 7)) << 4), k + 4);
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
 #pragma unroll
@@ -402,16 +416,16 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
       }
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks) {  // 16 keys
-        const int r = 32 * part + 16 * ks + (lane & 7) + (lane & 8), c = lane >> 4;
+        const int r = 32 * part + 16 * ks + (lane & 7) + (lane & 8), ch = lane >> 4;
 #pragma unroll
         for (int j = 0; j < (kF8 ? 2 : 4); ++j) {
           uint32_t v[4];
           if constexpr (kF8) {
-            ldsm4_t(sv + r * kRow + (((2 * j + c) ^ ((r >> 1) & 3)) << 4), v);
+            ldsm4_t(sv + r * kRow + (((2 * j + ch) ^ ((r >> 1) & 3)) << 4), v);
 #pragma unroll
             for (int u = 0; u < 4; ++u) v[u] = __byte_perm(v[u], 0u, 0x3120);
           } else {
-            ldsm4_t(sv + r * kRow + (((2 * j + c) ^ (r & 7)) << 4), v);
+            ldsm4_t(sv + r * kRow + (((2 * j + ch) ^ (r & 7)) << 4), v);
           }
 #pragma unroll
           for (int mt = 0; mt < kMT; ++mt) {
@@ -436,9 +450,9 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
 
     const bool unit_end = off + 1 == blocks;
     if (unit_end || i + 1 == count) {
-      // ---------------------------------------------- end of this piece of the unit
+      // ------------------------------------------- end of this piece of the request
       whole = whole && unit_end;
-      const int slot = 2 * worker + (unit_end ? 0 : 1);
+      const int slot = (2 * worker + (unit_end ? 0 : 1)) * p.per_chunk + hw;
       const float vs = kF8 ? __ldg(p.v_scale + g) : 1.f;
 #pragma unroll
       for (int mt = 0; mt < kMT; ++mt) {
@@ -449,7 +463,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
           sum += __shfl_xor_sync(0xffffffffu, sum, 1);
           sum += __shfl_xor_sync(0xffffffffu, sum, 2);
           const int t = row / p.G;
-          const bool valid = t < rq.n;
+          const bool valid = t < rq.n && real;
           const int head = valid ? g * p.G + row - t * p.G : 0;
           float f = vs;
           if (whole) {
@@ -471,16 +485,16 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
           __nv_bfloat16* dst = p.out + (static_cast<long long>(rq.t0 + t) * p.Hq + head) * kHeadDim;
           float* part = p.part_o + (static_cast<long long>(slot) * kR + row) * kHeadDim;
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
+          for (int e = 0; e < 4; ++e) {
             // 16 dims: two MMA tiles, side by side (bf16) or even and odd dims (e4m3).
-            const float y0 = o[mt][2 * c][2 * h] * f, y1 = o[mt][2 * c][2 * h + 1] * f;
-            const float z0 = o[mt][2 * c + 1][2 * h] * f, z1 = o[mt][2 * c + 1][2 * h + 1] * f;
+            const float y0 = o[mt][2 * e][2 * h] * f, y1 = o[mt][2 * e][2 * h + 1] * f;
+            const float z0 = o[mt][2 * e + 1][2 * h] * f, z1 = o[mt][2 * e + 1][2 * h + 1] * f;
             if constexpr (kF8) {
-              const int d = 16 * c + 4 * t4;
+              const int d = 16 * e + 4 * t4;
               if (whole) *reinterpret_cast<uint2*>(dst + d) = make_uint2(pack_bf16x2(y0, z0), pack_bf16x2(y1, z1));
               else *reinterpret_cast<float4*>(part + d) = make_float4(y0, z0, y1, z1);
             } else {
-              const int d = 16 * c + 2 * t4;
+              const int d = 16 * e + 2 * t4;
               if (whole) {
                 *reinterpret_cast<uint32_t*>(dst + d) = pack_bf16x2(y0, y1);
                 *reinterpret_cast<uint32_t*>(dst + d + 8) = pack_bf16x2(z0, z1);
@@ -493,20 +507,20 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
         }
       }
       if (unit_end && !whole) {
-        // The last piece of a cut unit: the first one belongs to the last
-        // worker whose piece begins at or before the unit's first block.
-        const long long begin = static_cast<long long>(pre[b]) * p.Hkv + static_cast<long long>(g) * blocks;
+        // The last piece of a cut request: the first one belongs to the last
+        // worker whose piece begins at or before the request's first block.
+        const long long begin = static_cast<long long>(pre[b]) * p.chunks + static_cast<long long>(c) * blocks;
         int w0 = min(static_cast<int>(begin * axis.workers / axis.total), worker - 1);
         while (w0 > 0 && axis.cut<kSnap>(w0) > begin) --w0;
         while (axis.cut<kSnap>(w0 + 1) <= begin) ++w0;
-        unit = make_int4(b, g, w0, 0);
+        unit = make_int4(b, c, w0, 0);
       }
       seg_begin = true;
     }
     if (unit_end) {
       off = 0;
-      if (++g == p.Hkv) {
-        g = 0;
+      if (++c == p.chunks) {
+        c = 0;
         if (i + 1 < count) {
           do ++b; while (pre[b + 1] == pre[b]);
           blocks = pre[b + 1] - pre[b];
@@ -527,25 +541,27 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
       }
     }
   }
-  if (p.part_unit && lane == 0) p.part_unit[worker] = unit;
+  if (reports) p.part_unit[worker] = unit;
 }
 
-// Joins the pieces of every cut unit and adds the sink: with M = max(s, max_k m_k),
+// Joins the pieces of every cut request and adds the sink: with M = max(s, max_k m_k),
 //   l = e^{s-M} + sum_k l_k e^{m_k-M},  out = sum_k O_k e^{m_k-M} / l,  lse = M + ln l.
-// One CTA per worker, whose work is the unit that worker completed (mostly
-// none); one warp per query row, half a warp per piece.
+// One CTA per worker and head of a chunk, whose work is the request that the
+// worker completed (mostly none); one warp per query row, half a warp per piece.
 template <int kR>
 __global__ void __launch_bounds__(256) sink_attn_paged_join_kernel(const __grid_constant__ PagedParams p) {
   pdl_wait();
-  const int4 unit = __ldcg(p.part_unit + blockIdx.x);
-  if (unit.x < 0) return;
-  const int last = blockIdx.x, pieces = last - unit.z + 1;
+  const int last = blockIdx.x, hw = blockIdx.y;
+  const int4 unit = __ldcg(p.part_unit + last);
+  const int g = unit.y * p.per_chunk + hw;
+  if (unit.x < 0 || g >= p.Hkv) return;
+  const int pieces = last - unit.z + 1;
   const PagedRequest rq = paged_request(p, unit.x);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  auto slot = [&](int k) { return k + 1 == pieces ? 2 * last : 2 * (unit.z + k) + 1; };
+  auto slot = [&](int k) { return (k + 1 == pieces ? 2 * last : 2 * (unit.z + k) + 1) * p.per_chunk + hw; };
   for (int row = warp; row < rq.n * p.G; row += 8) {
     const int t = row / p.G;
-    const int head = unit.y * p.G + row - t * p.G;
+    const int head = g * p.G + row - t * p.G;
     const float s2 = __ldg(p.sinks + head) * kLog2e;
     float top = s2;
     for (int k = lane; k < pieces; k += 32) top = fmaxf(top, __ldcg(p.part_ml + slot(k) * kR + row).x);
@@ -559,18 +575,24 @@ __global__ void __launch_bounds__(256) sink_attn_paged_join_kernel(const __grid_
       if (k0 + lane < pieces) ml = __ldcg(p.part_ml + slot(k0 + lane) * kR + row);
       const float f = ex2_approx(ml.x - ref);
       l = fmaf(ml.y, f, l);
-#pragma unroll 8
-      for (int k = 0; k < 32; k += 2) {
-        if (k0 + k >= pieces) break;
-        const int mine = k + (lane >> 4);
-        const float fk = __shfl_sync(0xffffffffu, f, mine);
-        if (k0 + mine < pieces) {
-          const float4 v = __ldcg(reinterpret_cast<const float4*>(
-              p.part_o + (static_cast<long long>(slot(k0 + mine)) * kR + row) * kHeadDim) + (lane & 15));
-          y.x = fmaf(v.x, fk, y.x);
-          y.y = fmaf(v.y, fk, y.y);
-          y.z = fmaf(v.z, fk, y.z);
-          y.w = fmaf(v.w, fk, y.w);
+      // Four pieces of each half warp at a time, their loads in flight together.
+      for (int k = 0; k < 32 && k0 + k < pieces; k += 8) {
+        float4 v[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int mine = k0 + k + 2 * u + (lane >> 4);
+          v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (mine < pieces)
+            v[u] = __ldcg(reinterpret_cast<const float4*>(p.part_o + (static_cast<long long>(slot(mine)) * kR + row) * kHeadDim) +
+                          (lane & 15));
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const float fk = __shfl_sync(0xffffffffu, f, k + 2 * u + (lane >> 4));
+          y.x = fmaf(v[u].x, fk, y.x);
+          y.y = fmaf(v[u].y, fk, y.y);
+          y.z = fmaf(v[u].z, fk, y.z);
+          y.w = fmaf(v[u].w, fk, y.w);
         }
       }
     }

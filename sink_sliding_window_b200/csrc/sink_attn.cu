@@ -678,7 +678,7 @@ PagedSplit split_paged(const sink_attn_paged_dims* d) {
 }
 
 constexpr int kPagedCtas = 148;  // one CTA per SM of a B200
-constexpr int kPagedWorkers = kPagedCtas * kRowsWarps;
+constexpr int kPagedWarps = kPagedCtas * kRowsWarps;
 
 // Workspace of a call (bytes): the pieces of cut units.
 struct PagedWorkspace {
@@ -688,9 +688,9 @@ struct PagedWorkspace {
 PagedWorkspace paged_workspace(const PagedSplit& s) {
   PagedWorkspace w = {0, 0, 0, 256};
   if (s.rows) {
-    w.ml = round256(kPagedWorkers * sizeof(int4));
-    w.o = w.ml + round256(kPagedWorkers * 2 * static_cast<size_t>(s.kR) * sizeof(float2));
-    w.total = w.o + kPagedWorkers * 2 * static_cast<size_t>(s.kR) * kHeadDim * sizeof(float);
+    w.ml = round256(kPagedWarps * sizeof(int4));
+    w.o = w.ml + round256(kPagedWarps * 2 * static_cast<size_t>(s.kR) * sizeof(float2));
+    w.total = w.o + kPagedWarps * 2 * static_cast<size_t>(s.kR) * kHeadDim * sizeof(float);
   }
   return w;
 }
@@ -742,7 +742,7 @@ bool launch_rows(PagedParams& p, const sink_attn_paged_dims* d, const void* k_ca
   if (cudaPeekAtLastError() != cudaSuccess) return false;
   if (!join) return true;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(kPagedWorkers, 1, 1);
+  cfg.gridDim = dim3(kPagedCtas * (kRowsWarps / p.per_chunk), p.per_chunk, 1);
   cfg.blockDim = dim3(256, 1, 1);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
@@ -793,6 +793,8 @@ sink_attn_status paged_attn_impl(const sink_attn_paged_dims* d, const void* q, c
   p.max_pages = d->max_pages;
   p.box_log2 = 0;
   p.few = split.few;
+  p.chunks = (p.Hkv + kRowsWarps - 1) / kRowsWarps;
+  p.per_chunk = (p.Hkv + p.chunks - 1) / p.chunks;
   p.window = window > 0 ? window : 0;
   p.scale_log2 = scale * kLog2e;
   p.q_stride = d->q_stride;
