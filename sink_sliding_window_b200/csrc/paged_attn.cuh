@@ -27,11 +27,12 @@ struct PagedParams {
   float* lse;
   // The few-rows kernel: key/value heads in chunks, and its workspace, per
   // worker two partial results for each head of a chunk (unnormalised O,
-  // reference max, sum) and which request it completes.
+  // reference max, sum), the cut request (and chunk) that its piece completes,
+  // and whether a request that it does not complete begins in its piece.
   int chunks, per_chunk;
   float* part_o;     // [workers][2][per_chunk][kR][64]
   float2* part_ml;   // [workers][2][per_chunk][kR] (m in log2 units, l)
-  int4* part_unit;   // [workers] (b or -1, chunk, first worker, 0)
+  int4* part_unit;   // [workers] (b or -1, chunk, begins, 0)
 };
 
 // One request's rows and keys.  Lengths that do not fit the call's sizes are

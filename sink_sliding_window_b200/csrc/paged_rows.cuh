@@ -1,18 +1,22 @@
 // Paged attention of requests with few query rows (single tokens above all):
 // the keys and values of a request cross HBM once, and that is what bounds it.
 //
-// A request's visible keys are cut into blocks of kKeys keys.  The blocks of
-// all requests, in order, are one axis, of which every worker takes an equal
+// A request's visible keys are cut into blocks of 32 keys
+// (e4m3: 64).  The blocks of all
+// requests, in order, are one axis, of which every worker takes an equal
 // piece: no share depends on how ragged the lengths are, and the host needs to
 // know none of them.  A worker is a group of warps, one for each of up to
-// eight key/value heads: the heads of a token lie side by side in most caches,
-// so that warps which read the same tokens at about the same time read whole
-// DRAM pages (with the heads one after another on the axis instead, the same
-// tokens crossed HBM 1.3 times, and 64 x 6-8k took 219 us for 142 us of
-// bytes).  The warps of a worker share nothing else: each fetches its blocks
-// with TMA into a ring of its own in shared memory, kStages blocks ahead, and
-// keeps running maximum, sum and O of its n * G query rows (n new tokens, G
-// heads; one or two 16-row MMA tiles) in registers.  The tiles come to the tensor cores through
+// eight key/value heads.  One TMA box holds a block's tokens of all the
+// worker's heads (dims ordered so that it lands head by head), which reads
+// whole rows of DRAM and costs one thread two instructions a block; a warp of
+// its own for the copies feeds the CTA's workers in turn, kRowsStages blocks
+// ahead, with the page numbers looked up a batch ahead.  (With the heads one
+// after another on the axis the same DRAM pages were opened 1.3 times and 64
+// requests of 6-8k took 219 us; with every warp fetching its own head's boxes
+// the issue took 570 of a block's 1650 cycles, 900 of 2700 for e4m3.)
+// A warp keeps running maximum, sum and O of its head's n * G query rows (n
+// new tokens, G heads; one or two 16-row MMA tiles) in registers, and shares
+// nothing with the others.  The tiles come to the tensor cores through
 // mma.sync: with 8 or 16 rows the S and P of a block are a few registers, and
 // the trip through tensor memory that the 128-row instructions need costs more
 // than the multiplication (the decode kernel over linear caches makes that
@@ -40,27 +44,32 @@
 
 namespace sa {
 
-constexpr int kRowsWarps = 8;
-constexpr int kRowsThreads = 32 * kRowsWarps;
+template <bool kF8>
+constexpr int kRowsKeys = kF8 ? 64 : 32;  // keys of a block: 4 KB of K, 4 KB of V for each head
 constexpr int kRowsStages = 3;
-constexpr int kRowsTile = 4096;  // bytes of a K or a V block: 32 bf16 keys or 64 e4m3 keys
-constexpr int kRowsRing = kRowsStages * 2 * kRowsTile;
 constexpr int kRowsMaxRows = 32;
+constexpr int kRowsHeads = 8;  // key/value heads of a chunk, at most
 // A cut closer than this many blocks to a request's end moves there: joining a
 // piece costs more than reading so few keys.
 template <bool kF8>
 constexpr int kRowsSnap = kF8 ? 1 : 2;
-template <bool kF8>
-constexpr int kRowsKeys = kF8 ? 64 : 32;
+// Fewest blocks of a worker.
+constexpr int kRowsMinBlocks = 4;
+constexpr int kRowsWarps = 8;  // that compute, of the one CTA of an SM
+constexpr int kRowsThreads = 32 * (kRowsWarps + 1);
+constexpr int kRowsTile = 4096;  // bytes of one head's K or V block
 
 struct RowsCtl {
-  uint64_t full[kRowsWarps][kRowsStages];
+  uint64_t full[kRowsWarps][kRowsStages];   // [worker of the CTA][stage]
+  uint64_t empty[kRowsWarps][kRowsStages];
   int abort;
-  int sums[kRowsWarps];
+  int sums[kRowsWarps + 1];
+  int4 cuts[kRowsWarps + 1];  // where the pieces of the CTA's workers begin, and the last one ends: x, b, c, off
 };
 
 constexpr size_t rows_smem_bytes(int batch) {
-  return 1024 + kRowsWarps * kRowsRing + sizeof(RowsCtl) + (static_cast<size_t>(batch) + 1) * sizeof(int);
+  return 1024 + kRowsWarps * kRowsStages * 2 * kRowsTile + sizeof(RowsCtl) +
+         (static_cast<size_t>(batch) + 1) * sizeof(int);
 }
 
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t* r) {
@@ -78,53 +87,83 @@ __device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t* r) {
 template <bool kF16>
 __device__ __forceinline__ void mma_16816(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
   if constexpr (kF16)
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
   else
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
 // First key (a multiple of the TMA box) and number of blocks of a request's units.
-template <bool kF8>
 __device__ __forceinline__ int rows_first(const PagedParams& p, const PagedRequest& r) {
   return r.lo >> p.box_log2 << p.box_log2;
 }
 template <bool kF8>
 __device__ __forceinline__ int rows_blocks(const PagedParams& p, const PagedRequest& r) {
   if (r.n == 0 || r.n > p.few) return 0;
-  return max(1, (r.len - rows_first<kF8>(p, r) + kRowsKeys<kF8> - 1) / kRowsKeys<kF8>);
+  return max(1, (r.len - rows_first(p, r) + kRowsKeys<kF8> - 1) / kRowsKeys<kF8>);
 }
 
-// The axis of all blocks: request by request, and within it chunk by chunk of
-// its key/value heads (one chunk when there are at most kRowsWarps heads).
+// A place on the axis of all blocks: block `off` of a request and a chunk of
+// its key/value heads.
+struct RowsAt {
+  uint32_t x;
+  int b, c, off;
+};
+
+// The axis: request by request, and within it chunk by chunk of its heads (one
+// chunk when there are at most kRowsHeads).  Its functions are called by whole
+// warps.
+template <int kSnap>
 struct RowsAxis {
   const int* pre;  // blocks before request b (of one chunk), [batch + 1]
   int batch, chunks;
-  long long total;
-  int workers;
+  uint32_t total, workers;
 
-  __device__ __forceinline__ int find(long long x) const {  // the request of block x < total
-    const int q = static_cast<int>(x / chunks);
-    int lo = 0, hi = batch - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (pre[mid] <= q) lo = mid; else hi = mid - 1;
+  // The last request whose blocks begin at or before q.
+  __device__ __forceinline__ int find(int q) const {
+    const int lane = lane_id();
+    int lo = 0, n = batch;
+    while (n > 1) {
+      const int step = (n + 31) >> 5;
+      const bool le = lane * step < n && pre[lo + lane * step] <= q;
+      const int k = (__popc(__ballot_sync(0xffffffffu, le)) - 1) * step;
+      lo += k;
+      n = min(step, n - k);
     }
     return lo;
   }
+  __device__ __forceinline__ int blocks(int b) const { return pre[b + 1] - pre[b]; }
+  // Moves on to the next chunk, or the next request that has blocks.
+  __device__ __forceinline__ void next_unit(RowsAt& a) const {
+    a.off = 0;
+    if (++a.c < chunks) return;
+    a.c = 0;
+    do ++a.b; while (a.b < batch && blocks(a.b) == 0);
+  }
   // Where worker w's piece begins.
-  template <int kSnap>
-  __device__ __forceinline__ long long cut(int w) const {
-    const long long x = w * total / workers;
-    if (w >= workers || x >= total) return total;
-    const int b = find(x);
-    const int blocks = pre[b + 1] - pre[b];
-    const int off = static_cast<int>((x - static_cast<long long>(pre[b]) * chunks) % blocks);
-    if (off <= kSnap) return x - off;
-    return blocks - off <= kSnap ? x + blocks - off : x;
+  __device__ __forceinline__ RowsAt cut(uint32_t w) const {
+    RowsAt a = {total, batch, 0, 0};
+    if (w >= workers) return a;
+    const uint32_t share = total / workers, rest = total - share * workers;
+    a.x = w * share + w * rest / workers;
+    uint32_t q = a.x;
+    if (chunks > 1) q /= chunks;
+    a.b = find(static_cast<int>(q));
+    const uint32_t n = blocks(a.b);
+    const uint32_t in = a.x - static_cast<uint32_t>(pre[a.b]) * chunks;
+    a.c = chunks > 1 ? in / n : 0;
+    a.off = in - a.c * n;
+    if (a.off <= kSnap) {
+      a.x -= a.off;
+      a.off = 0;
+    } else if (static_cast<int>(n) - a.off <= kSnap) {
+      a.x += n - a.off;
+      next_unit(a);
+    }
+    return a;
   }
 };
 
@@ -132,22 +171,31 @@ template <bool kF8, int kR>
 __global__ void __launch_bounds__(kRowsThreads, 1)
     sink_attn_paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                                 const __grid_constant__ PagedParams p) {
+  constexpr int kWarps = kRowsWarps;
+  constexpr int kThreads = kRowsThreads;
+  constexpr int kTile = kRowsTile;
   constexpr int kKeys = kRowsKeys<kF8>;
+  // Keys of one softmax step: all of a block where registers allow it.
+  constexpr int kStep = kF8 && kR <= 16 ? 64 : 32;
+  constexpr int kNT = kStep / 8;
   constexpr int kRow = kF8 ? 64 : 128;         // bytes of a key row in shared memory
   constexpr int kMT = kR == 32 ? 2 : 1;        // 16-row MMA tiles
   constexpr int kHalves = kR == 8 ? 1 : 2;     // 8-row halves of a tile that hold rows
-  constexpr int kSnap = kRowsSnap<kF8>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align1024(smem_raw);
-  RowsCtl* ctl = reinterpret_cast<RowsCtl*>(smem + kRowsWarps * kRowsRing);
+  RowsCtl* ctl = reinterpret_cast<RowsCtl*>(smem + kWarps * kRowsStages * 2 * kTile);
   int* pre = reinterpret_cast<int*>(ctl + 1);
   volatile int* abort = &ctl->abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_launch_dependents();  // the combine kernel waits for this one's end by itself
 
+  const int groups = kWarps / p.per_chunk;  // workers of this CTA
   if (threadIdx.x == 0) {
-    for (int w = 0; w < kRowsWarps; ++w)
-      for (int s = 0; s < kRowsStages; ++s) mbar_init(&ctl->full[w][s], 1);
+    for (int w = 0; w < groups; ++w)
+      for (int s = 0; s < kRowsStages; ++s) {
+        mbar_init(&ctl->full[w][s], 1);
+        mbar_init(&ctl->empty[w][s], p.per_chunk);
+      }
     ctl->abort = 0;
     fence_mbar_init();
     tma_prefetch_desc(&tm_k);
@@ -155,7 +203,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
   }
   // pre[]: every CTA sums the requests' blocks for itself.
   {
-    const int per = (p.batch + kRowsThreads - 1) / kRowsThreads;
+    const int per = (p.batch + kThreads - 1) / kThreads;
     const int b0 = threadIdx.x * per;
     int sum = 0;
     for (int i = 0; i < per; ++i) {
@@ -186,85 +234,127 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
     __syncthreads();
   }
 
-  RowsAxis axis;
+  RowsAxis<kRowsSnap<kF8>> axis;
   axis.pre = pre;
   axis.batch = p.batch;
   axis.chunks = p.chunks;
-  axis.total = static_cast<long long>(pre[p.batch]) * p.chunks;
-  const int per_cta = kRowsWarps / p.per_chunk;  // workers
-  axis.workers = static_cast<int>(min(static_cast<long long>(gridDim.x) * per_cta, axis.total));
-  const int hw = warp % p.per_chunk;  // this warp's head within its chunk
-  if (warp >= per_cta * p.per_chunk) return;
-  const int worker = blockIdx.x * per_cta + warp / p.per_chunk;
+  axis.total = static_cast<uint32_t>(pre[p.batch]) * p.chunks;
+  axis.workers = min(gridDim.x * groups, (axis.total + kRowsMinBlocks - 1) / kRowsMinBlocks);
+
+  for (int g = warp; g <= groups; g += kWarps + 1) {
+    const RowsAt a = axis.cut(blockIdx.x * groups + g);
+    if (lane == 0) ctl->cuts[g] = make_int4(static_cast<int>(a.x), a.b, a.c, a.off);
+  }
+  __syncthreads();
+  auto cut_of = [&](int g) {
+    const int4 v = ctl->cuts[g];
+    return RowsAt{static_cast<uint32_t>(v.x), v.y, v.z, v.w};
+  };
+
+  const uint32_t group_bytes = p.per_chunk * kRowsStages * 2 * kTile, stage_bytes = p.per_chunk * 2 * kTile;
+  if (warp == kWarps) {
+    // ------------------------------------------------------------------ copies
+    // Lanes lpg * g .. of the warp keep the state of worker g and, one per
+    // box, the page numbers of a batch of its next blocks; the batch after it
+    // is looked up while this one is copied.
+    const int nbox_log2 = (kF8 ? 6 : 5) - p.box_log2, nbox = 1 << nbox_log2, lpg = 32 / groups;
+    const int mine = min(lane / lpg, groups - 1), li = lane - mine * lpg;
+    RowsAt at = cut_of(mine);
+    const int count = static_cast<int>(cut_of(mine + 1).x - at.x);
+    int left = count;
+    struct Batch {
+      int n, c, key, entry;  // blocks, chunk, first key, this lane's table entry
+      bool want;
+    };
+    auto look_up = [&]() {
+      Batch t = {0, 0, 0, 0, false};
+      if (left == 0) return t;
+      const PagedRequest r = paged_request(p, at.b);
+      const int blocks = axis.blocks(at.b);
+      t.n = min(min(lpg / nbox, blocks - at.off), left);
+      t.c = at.c;
+      t.key = rows_first(p, r) + at.off * kKeys;
+      const int j = t.key + (li << p.box_log2);
+      t.want = li < t.n * nbox && j < r.len;
+      if (t.want) t.entry = paged_entry(p, at.b, j);
+      left -= t.n;
+      at.off += t.n;
+      if (at.off == blocks) axis.next_unit(at);
+      return t;
+    };
+    Batch now = look_up(), next = look_up();
+    int j = 0, page = now.want ? paged_page(p, now.entry) : p.num_pages;
+    const int most = __reduce_max_sync(0xffffffffu, count);
+    bool ok = true;
+    for (int i = 0; ok && i < most; ++i) {
+      const int s = i % kRowsStages;
+      if (j == now.n) {
+        now = next;
+        page = now.want ? paged_page(p, now.entry) : p.num_pages;
+        next = look_up();
+        j = 0;
+      }
+      __syncwarp();
+      for (int g = 0; ok && g < groups; ++g) {
+        const int src = g * lpg;
+        const int jg = __shfl_sync(0xffffffffu, j, src);
+        const int key = __shfl_sync(0xffffffffu, now.key, src) + jg * kKeys;
+        const int head = __shfl_sync(0xffffffffu, now.c, src) * p.per_chunk;
+        int pages[kKeys / 16];
+#pragma unroll
+        for (int x = 0; x < kKeys / 16; ++x) pages[x] = __shfl_sync(0xffffffffu, page, src + jg * nbox + min(x, nbox - 1));
+        if (i >= __shfl_sync(0xffffffffu, count, src)) continue;
+        if (i >= kRowsStages)
+          ok = warp_all(mbar_wait(&ctl->empty[g][s], ((i / kRowsStages) - 1) & 1, abort, &g_device_error,
+                                  kDevErrTimeoutProducer));
+        if (ok && elect_one()) {
+          uint64_t* full = &ctl->full[g][s];
+          uint8_t* dst = smem + g * group_bytes + s * stage_bytes;
+          mbar_arrive_expect_tx(full, stage_bytes);
+#pragma unroll
+          for (int x = 0; x < kKeys / 16; ++x) {
+            if (x >= nbox) break;
+            const int in_page = (key + (x << p.box_log2)) & ((1 << p.page_log2) - 1);
+            uint8_t* to = dst + x * (stage_bytes / 2 >> nbox_log2);
+            tma_load_4d(to, &tm_k, full, 0, in_page, head, pages[x]);
+            tma_load_4d(to + stage_bytes / 2, &tm_v, full, 0, in_page, head, pages[x]);
+          }
+        }
+        __syncwarp();
+      }
+      ++j;
+    }
+    return;
+  }
+
+  // ----------------------------------------------------------------- attention
+  if (warp >= groups * p.per_chunk) return;
+  const int group = warp / p.per_chunk, hw = warp - group * p.per_chunk;  // worker of the CTA, head of its chunk
+  const int worker = blockIdx.x * groups + group;
   const bool reports = p.part_unit && hw == 0 && lane == 0;
-  int4 unit = make_int4(-1, 0, 0, 0);  // the cut request (and chunk) that this worker completes
-  const long long x0 = worker < axis.workers ? axis.cut<kSnap>(worker) : 0;
-  const int count = worker < axis.workers ? static_cast<int>(axis.cut<kSnap>(worker + 1) - x0) : 0;
+  int4 unit = make_int4(-1, 0, 0, 0);  // see PagedParams::part_unit
+  RowsAt at = cut_of(group);
+  const int count = static_cast<int>(cut_of(group + 1).x - at.x);
   if (count == 0) {
     if (reports) p.part_unit[worker] = unit;
     return;
   }
-
-  // The request and chunk of the block that is computed next.
-  int b = axis.find(x0);
-  int blocks = pre[b + 1] - pre[b];
-  int c = static_cast<int>((x0 - static_cast<long long>(pre[b]) * p.chunks) / blocks);
-  int off = static_cast<int>((x0 - static_cast<long long>(pre[b]) * p.chunks) % blocks);
-  PagedRequest rq = paged_request(p, b);
-  int first = rows_first<kF8>(p, rq);
-
-  // The same of the block that is fetched next; its pages are looked up one
-  // block ahead of the copy.  (The last chunk may have fewer heads: a warp
-  // without one reads the last head and writes nothing.)
-  auto head_of = [&](int chunk) { return min(chunk * p.per_chunk + hw, p.Hkv - 1); };
-  int fb = b, fc = c, foff = off, fblocks = blocks, flen = rq.len, ffirst = first, fetched = 0;
-  uint8_t* ring = smem + warp * kRowsRing;
-  uint64_t* full = ctl->full[warp];
-  const int nbox = kKeys >> p.box_log2;
-  const int page_mask = (1 << p.page_log2) - 1;
-  int next_page = 0, next_at = 0, next_g = 0;
-  bool next_want = false;
-  auto lookup = [&]() {
-    const int j = ffirst + foff * kKeys + (lane << p.box_log2);
-    // Looked at by fetch(), so that the load is not waited for here.
-    next_want = lane < nbox && j < flen;
-    if (next_want) next_page = paged_entry(p, fb, j);
-    next_at = j & page_mask;
-    next_g = head_of(fc);
-    if (++foff == fblocks) {
-      foff = 0;
-      if (++fc == p.chunks) {
-        fc = 0;
-        if (fetched + 1 < count) {
-          do ++fb; while (pre[fb + 1] == pre[fb]);
-          fblocks = pre[fb + 1] - pre[fb];
-          const PagedRequest r = paged_request(p, fb);
-          flen = r.len;
-          ffirst = rows_first<kF8>(p, r);
-        }
-      }
-    }
-    ++fetched;
-  };
-  auto fetch = [&](int s) {  // the block looked up last, into stage s
-    if (lane == 0) mbar_arrive_expect_tx(&full[s], 2 * kRowsTile);
-    __syncwarp();
-    if (lane < nbox) {
-      uint8_t* dst = ring + s * 2 * kRowsTile + (lane << p.box_log2) * kRow;
-      const int page = next_want ? paged_page(p, next_page) : p.num_pages;
-      tma_load_4d(dst, &tm_k, &full[s], 0, next_g, next_at, page);
-      tma_load_4d(dst + kRowsTile, &tm_v, &full[s], 0, next_g, next_at, page);
-    }
-    if (fetched < count) lookup();
-  };
-  lookup();
-  for (int s = 0; s < kRowsStages && s < count; ++s) fetch(s);
+  PagedRequest rq = paged_request(p, at.b);
+  int first = rows_first(p, rq), blocks = axis.blocks(at.b);
+  const uint8_t* ring = smem + group * group_bytes;
+  uint64_t* full = ctl->full[group];
+  // Keys of this warp's head within a box, and the bytes from one box to the next.
+  const int box = 1 << p.box_log2, box_bytes = p.per_chunk * box * kRow;
+  const int head_bytes = hw * box * kRow;
 
   const int t4 = lane & 3, r8 = lane >> 2;
   uint32_t q[kMT][4][4];
   float o[kMT][8][4], m[kMT][2], l[kMT][2];
   int key_lo[kMT][2], key_hi[kMT][2];  // keys that this thread's rows see
-  bool seg_begin = true, whole = false, real = true;
+  bool seg_begin = true, whole = false;
+  // The last chunk may have fewer heads: a warp without one computes on zeros
+  // and writes nothing.
+  bool real = true;
   int g = 0;
   float sl2 = 0.f;
   bool ok = true;
@@ -273,9 +363,9 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
   for (int i = 0; i < count; ++i) {
     if (seg_begin) {
       seg_begin = false;
-      whole = off == 0;
-      g = head_of(c);
-      real = c * p.per_chunk + hw < p.Hkv;
+      whole = at.off == 0;
+      g = min(at.c * p.per_chunk + hw, p.Hkv - 1);
+      real = at.c * p.per_chunk + hw < p.Hkv;
       sl2 = kF8 ? p.scale_log2 * __ldg(p.k_scale + g) : p.scale_log2;
 #pragma unroll
       for (int mt = 0; mt < kMT; ++mt) {
@@ -316,8 +406,8 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
     done = i;
     ok = warp_all(mbar_wait(&full[s], (i / kRowsStages) & 1, abort, &g_device_error, kDevErrTimeoutDecode));
     if (!ok) break;
-    uint8_t* tile = ring + s * 2 * kRowsTile;
-    const int base = first + off * kKeys;
+    const uint8_t* tile = ring + s * stage_bytes;
+    const int base = first + at.off * kKeys;
     // Keys in front of the first visible one or behind the last: their slots
     // may hold any bits.  S is masked below; the values become zeros, since
     // 0 * NaN is not 0.
@@ -326,31 +416,34 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
 #pragma unroll
       for (int r = lane; r < kKeys; r += 32) {
         if (base + r < rq.lo || base + r >= rq.len) {
+          uint8_t* row = const_cast<uint8_t*>(tile) + stage_bytes / 2 + (r >> p.box_log2) * box_bytes + head_bytes +
+                         (r & (box - 1)) * kRow;
 #pragma unroll
-          for (int c = 0; c < kRow / 16; ++c)
-            *reinterpret_cast<uint4*>(tile + kRowsTile + r * kRow + 16 * c) = make_uint4(0u, 0u, 0u, 0u);
+          for (int ch = 0; ch < kRow / 16; ++ch) *reinterpret_cast<uint4*>(row + 16 * ch) = make_uint4(0u, 0u, 0u, 0u);
         }
       }
-      fence_proxy_async_smem();  // before the copy that reuses the stage
       __syncwarp();
     }
     // Any key of this block that some row does not see?
     const bool masked = base + kKeys - 1 > rq.len - rq.n || (p.window > 0 && base < rq.len - p.window);
-    const uint32_t sk = smem_u32(tile), sv = sk + kRowsTile;
+    const uint32_t sk = smem_u32(tile) + head_bytes, sv = sk + stage_bytes / 2;
+    // Where 16 keys of this warp's K lie: in a box of their own, or in one with others.
+    auto keys16 = [&](int k) -> uint32_t { return ((16 * k) >> p.box_log2) * box_bytes + ((16 * k) & (box - 1)) * kRow; };
 
 #pragma unroll
-    for (int part = 0; part < kKeys / 32; ++part) {  // 32 keys at a time
-      float x[kMT][4][4];
+    for (int step = 0; step < kKeys / kStep; ++step) {
+      float x[kMT][kNT][4];
 #pragma unroll
-      for (int nt = 0; nt < 4; ++nt) {
+      for (int nt = 0; nt < kNT; ++nt) {
 #pragma unroll
         for (int mt = 0; mt < kMT; ++mt)
 #pragma unroll
           for (int u = 0; u < 4; ++u) x[mt][nt][u] = 0.f;
-        const int r = 32 * part + 8 * nt + (lane & 7), ch = lane >> 3;
+        const int r = 8 * (nt & 1) + (lane & 7), ch = lane >> 3;
+        const uint32_t sk16 = sk + keys16(step * (kStep / 16) + (nt >> 1)) + r * kRow;
         if constexpr (kF8) {
           uint32_t k[4];
-          ldsm4(sk + r * kRow + ((ch ^ ((r >> 1) & 3)) << 4), k);
+          ldsm4(sk16 + ((ch ^ ((r >> 1) & 3)) << 4), k);
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
 #pragma unroll
@@ -358,8 +451,8 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
               mma_16816<true>(x[mt][nt], q[mt][kk], e4m3x2_to_f16x2(k[kk]), e4m3x2_to_f16x2(k[kk] >> 16));
         } else {
           uint32_t k[8];
-          ldsm4(sk + r * kRow + ((ch ^ (r & 7)) << 4), k);
-          ldsm4(sk + r * kRow + (((ch + 4) ^ (r & 7)) << 4), k + 4);
+          ldsm4(sk16 + ((ch ^ (r & 7)) << 4), k);
+          ldsm4(sk16 + (((ch + 4) ^ (r & 7)) << 4), k + 4);
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
 #pragma unroll
@@ -367,30 +460,30 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
         }
       }
       if (masked) {
-        const int j0 = base + 32 * part + 2 * t4;
+        const int j0 = base + kStep * step + 2 * t4;
 #pragma unroll
         for (int mt = 0; mt < kMT; ++mt)
 #pragma unroll
-          for (int nt = 0; nt < 4; ++nt)
+          for (int nt = 0; nt < kNT; ++nt)
 #pragma unroll
             for (int u = 0; u < 2 * kHalves; ++u) {
               const int j = j0 + 8 * nt + (u & 1);
               if (j < key_lo[mt][u >> 1] || j > key_hi[mt][u >> 1]) x[mt][nt][u] = -INFINITY;
             }
       }
-      uint32_t pk[kMT][4][2];
+      uint32_t pk[kMT][kNT][2];
 #pragma unroll
       for (int mt = 0; mt < kMT; ++mt) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           if (h >= kHalves) {
 #pragma unroll
-            for (int nt = 0; nt < 4; ++nt) pk[mt][nt][h] = 0u;
+            for (int nt = 0; nt < kNT; ++nt) pk[mt][nt][h] = 0u;
             continue;
           }
           float top = -INFINITY;
 #pragma unroll
-          for (int nt = 0; nt < 4; ++nt) top = fmax3(top, x[mt][nt][2 * h], x[mt][nt][2 * h + 1]);
+          for (int nt = 0; nt < kNT; ++nt) top = fmax3(top, x[mt][nt][2 * h], x[mt][nt][2 * h + 1]);
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2)) * sl2;
           const float old = m[mt][h];
@@ -405,7 +498,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
           const float ref = m[mt][h] == -INFINITY ? 0.f : m[mt][h];
           float sum = 0.f;
 #pragma unroll
-          for (int nt = 0; nt < 4; ++nt) {
+          for (int nt = 0; nt < kNT; ++nt) {
             const float e0 = ex2_approx(fmaf(x[mt][nt][2 * h], sl2, -ref));
             const float e1 = ex2_approx(fmaf(x[mt][nt][2 * h + 1], sl2, -ref));
             sum += e0 + e1;
@@ -415,17 +508,18 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
         }
       }
 #pragma unroll
-      for (int ks = 0; ks < 2; ++ks) {  // 16 keys
-        const int r = 32 * part + 16 * ks + (lane & 7) + (lane & 8), ch = lane >> 4;
+      for (int ks = 0; ks < kStep / 16; ++ks) {
+        const int r = (lane & 7) + (lane & 8), ch = lane >> 4;
+        const uint32_t sv16 = sv + keys16(step * (kStep / 16) + ks) + r * kRow;
 #pragma unroll
         for (int j = 0; j < (kF8 ? 2 : 4); ++j) {
           uint32_t v[4];
           if constexpr (kF8) {
-            ldsm4_t(sv + r * kRow + (((2 * j + ch) ^ ((r >> 1) & 3)) << 4), v);
+            ldsm4_t(sv16 + (((2 * j + ch) ^ ((r >> 1) & 3)) << 4), v);
 #pragma unroll
             for (int u = 0; u < 4; ++u) v[u] = __byte_perm(v[u], 0u, 0x3120);
           } else {
-            ldsm4_t(sv + r * kRow + (((2 * j + ch) ^ (r & 7)) << 4), v);
+            ldsm4_t(sv16 + (((2 * j + ch) ^ (r & 7)) << 4), v);
           }
 #pragma unroll
           for (int mt = 0; mt < kMT; ++mt) {
@@ -445,12 +539,15 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
         }
       }
     }
-    __syncwarp();  // every lane has read the stage
-    if (i + kRowsStages < count) fetch(s);
+    // This warp has read the stage, before the copy that reuses it.
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&ctl->empty[group][s]);
 
-    const bool unit_end = off + 1 == blocks;
+    const bool unit_end = at.off + 1 == blocks;
     if (unit_end || i + 1 == count) {
       // ------------------------------------------- end of this piece of the request
+      const bool begun = whole;
       whole = whole && unit_end;
       const int slot = (2 * worker + (unit_end ? 0 : 1)) * p.per_chunk + hw;
       const float vs = kF8 ? __ldg(p.v_scale + g) : 1.f;
@@ -506,38 +603,30 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
           }
         }
       }
-      if (unit_end && !whole) {
-        // The last piece of a cut request: the first one belongs to the last
-        // worker whose piece begins at or before the request's first block.
-        const long long begin = static_cast<long long>(pre[b]) * p.chunks + static_cast<long long>(c) * blocks;
-        int w0 = min(static_cast<int>(begin * axis.workers / axis.total), worker - 1);
-        while (w0 > 0 && axis.cut<kSnap>(w0) > begin) --w0;
-        while (axis.cut<kSnap>(w0 + 1) <= begin) ++w0;
-        unit = make_int4(b, c, w0, 0);
-      }
+      if (unit_end && !whole) unit.x = at.b, unit.y = at.c;
+      if (!unit_end && begun) unit.z = 1;
       seg_begin = true;
     }
     if (unit_end) {
-      off = 0;
-      if (++c == p.chunks) {
-        c = 0;
-        if (i + 1 < count) {
-          do ++b; while (pre[b + 1] == pre[b]);
-          blocks = pre[b + 1] - pre[b];
-          rq = paged_request(p, b);
-          first = rows_first<kF8>(p, rq);
+      if (i + 1 < count) {
+        const int last = at.b;
+        axis.next_unit(at);
+        if (at.b != last) {
+          blocks = axis.blocks(at.b);
+          rq = paged_request(p, at.b);
+          first = rows_first(p, rq);
         }
       }
     } else {
-      ++off;
+      ++at.off;
     }
   }
   if (!ok) {
-    unit.x = -1;
-    // The copies in flight still write to this CTA's shared memory.
+    unit = make_int4(-1, 0, 0, 0);
+    // Copies in flight still write to this CTA's shared memory.
     for (int i = done; i < min(count, done + kRowsStages); ++i) {
       const uint64_t t0 = global_timer_ns();
-      while (!mbar_try_wait(&full[i % kRowsStages], (i / kRowsStages) & 1) && global_timer_ns() - t0 < kWaitLimitNs) {
+      while (!mbar_try_wait(&full[i % kRowsStages], (i / kRowsStages) & 1) && global_timer_ns() - t0 < kWaitLimitNs / 4) {
       }
     }
   }
@@ -547,68 +636,114 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
 // Joins the pieces of every cut request and adds the sink: with M = max(s, max_k m_k),
 //   l = e^{s-M} + sum_k l_k e^{m_k-M},  out = sum_k O_k e^{m_k-M} / l,  lse = M + ln l.
 // One CTA per worker and head of a chunk, whose work is the request that the
-// worker completed (mostly none); one warp per query row, half a warp per piece.
+// worker completed (mostly none).  Its warps take the pieces in turn, eight
+// rows at a time (a lane holds four rows' four dims), then join their own
+// eight results in shared memory in the same way.
 template <int kR>
-__global__ void __launch_bounds__(256) sink_attn_paged_join_kernel(const __grid_constant__ PagedParams p) {
+__global__ void __launch_bounds__(256, 3) sink_attn_paged_join_kernel(const __grid_constant__ PagedParams p) {
+  __shared__ float s_o[8][8][kHeadDim];
+  __shared__ float s_m[8][8], s_l[8][8];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_wait();
   const int last = blockIdx.x, hw = blockIdx.y;
   const int4 unit = __ldcg(p.part_unit + last);
   const int g = unit.y * p.per_chunk + hw;
   if (unit.x < 0 || g >= p.Hkv) return;
-  const int pieces = last - unit.z + 1;
+  // The first piece is that of the nearest worker before this one whose last
+  // piece begins a request.
   const PagedRequest rq = paged_request(p, unit.x);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  auto slot = [&](int k) { return (k + 1 == pieces ? 2 * last : 2 * (unit.z + k) + 1) * p.per_chunk + hw; };
-  for (int row = warp; row < rq.n * p.G; row += 8) {
-    const int t = row / p.G;
-    const int head = g * p.G + row - t * p.G;
-    const float s2 = __ldg(p.sinks + head) * kLog2e;
-    float top = s2;
-    for (int k = lane; k < pieces; k += 32) top = fmaxf(top, __ldcg(p.part_ml + slot(k) * kR + row).x);
+  int start = last;
+  for (bool found = false; !found && start > 0;) {
+    const int w = start - 1 - lane;
+    const uint32_t begins = __ballot_sync(0xffffffffu, w >= 0 && __ldcg(&p.part_unit[max(w, 0)].z) != 0);
+    found = begins != 0;
+    start = found ? start - __ffs(begins) : max(0, start - 32);
+  }
+  const int pieces = last - start + 1;
+  auto slot = [&](int k) { return (k + 1 == pieces ? 2 * last : 2 * (start + k) + 1) * p.per_chunk + hw; };
+  const int rows = rq.n * p.G;
+  for (int r0 = 0; r0 < rows; r0 += 8) {
+    // This lane's rows r0 + (lane >> 4) + 2 u, u < 4, and dims 4 (lane & 15) ..; a
+    // piece's rows behind the last one are in the workspace, and never used.
+    float m[4], l[4];
+    float4 y[4];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    const float ref = top == -INFINITY ? 0.f : top;
-    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-    float l = 0.f;
-    for (int k0 = 0; k0 < pieces; k0 += 32) {
-      float2 ml = make_float2(-INFINITY, 0.f);
-      if (k0 + lane < pieces) ml = __ldcg(p.part_ml + slot(k0 + lane) * kR + row);
-      const float f = ex2_approx(ml.x - ref);
-      l = fmaf(ml.y, f, l);
-      // Four pieces of each half warp at a time, their loads in flight together.
-      for (int k = 0; k < 32 && k0 + k < pieces; k += 8) {
-        float4 v[4];
+    for (int u = 0; u < 4; ++u) m[u] = -INFINITY, l[u] = 0.f, y[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+    constexpr int kAtOnce = 2;
+    for (int k0 = warp; k0 < pieces; k0 += 8 * kAtOnce) {
+      float4 v[kAtOnce][4];
+      float2 ml[kAtOnce][4];
+#pragma unroll
+      for (int a = 0; a < kAtOnce; ++a) {
+        const int k = k0 + 8 * a;
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-          const int mine = k0 + k + 2 * u + (lane >> 4);
-          v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (mine < pieces)
-            v[u] = __ldcg(reinterpret_cast<const float4*>(p.part_o + (static_cast<long long>(slot(mine)) * kR + row) * kHeadDim) +
-                          (lane & 15));
+          const int row = r0 + (lane >> 4) + 2 * u;
+          ml[a][u] = make_float2(-INFINITY, 0.f);
+          if (k < pieces && row < rows) {
+            const long long at = static_cast<long long>(slot(k)) * kR + row;
+            ml[a][u] = __ldcg(p.part_ml + at);
+            v[a][u] = __ldcg(reinterpret_cast<const float4*>(p.part_o + at * kHeadDim) + (lane & 15));
+          } else {
+            v[a][u] = make_float4(0.f, 0.f, 0.f, 0.f);
+          }
         }
+      }
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const float fk = __shfl_sync(0xffffffffu, f, k + 2 * u + (lane >> 4));
-          y.x = fmaf(v[u].x, fk, y.x);
-          y.y = fmaf(v[u].y, fk, y.y);
-          y.z = fmaf(v[u].z, fk, y.z);
-          y.w = fmaf(v[u].w, fk, y.w);
+      for (int u = 0; u < 4; ++u) {
+        float now = m[u];
+#pragma unroll
+        for (int a = 0; a < kAtOnce; ++a) now = fmaxf(now, ml[a][u].x);
+        const float ref = now == -INFINITY ? 0.f : now;
+        const float f0 = ex2_approx(m[u] - ref);
+        m[u] = now;
+        l[u] *= f0;
+        y[u] = make_float4(y[u].x * f0, y[u].y * f0, y[u].z * f0, y[u].w * f0);
+#pragma unroll
+        for (int a = 0; a < kAtOnce; ++a) {
+          const float f = ex2_approx(ml[a][u].x - ref);
+          l[u] = fmaf(ml[a][u].y, f, l[u]);
+          y[u].x = fmaf(v[a][u].x, f, y[u].x);
+          y[u].y = fmaf(v[a][u].y, f, y[u].y);
+          y[u].z = fmaf(v[a][u].z, f, y[u].z);
+          y[u].w = fmaf(v[a][u].w, f, y[u].w);
         }
       }
     }
+    __syncthreads();  // the last rows have been read
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-    y.x += __shfl_xor_sync(0xffffffffu, y.x, 16);
-    y.y += __shfl_xor_sync(0xffffffffu, y.y, 16);
-    y.z += __shfl_xor_sync(0xffffffffu, y.z, 16);
-    y.w += __shfl_xor_sync(0xffffffffu, y.w, 16);
-    l += s2 == ref ? 1.f : ex2_approx(s2 - ref);
-    const float f = l > 0.f ? 1.f / l : 0.f;
-    if (lane < 16)
-      *reinterpret_cast<uint2*>(p.out + (static_cast<long long>(rq.t0 + t) * p.Hq + head) * kHeadDim + 4 * lane) =
-          make_uint2(pack_bf16x2(y.x * f, y.y * f), pack_bf16x2(y.z * f, y.w * f));
-    if (lane == 0)
-      p.lse[static_cast<long long>(head) * p.T + rq.t0 + t] = l > 0.f ? (ref + __log2f(l)) * kLn2 : -INFINITY;
+    for (int u = 0; u < 4; ++u) {
+      const int r = (lane >> 4) + 2 * u;
+      *reinterpret_cast<float4*>(&s_o[warp][r][4 * (lane & 15)]) = y[u];
+      if ((lane & 15) == 0) s_m[warp][r] = m[u], s_l[warp][r] = l[u];
+    }
+    __syncthreads();
+    // One warp per row, two dims per lane.
+    const int row = r0 + warp;
+    if (row < rows) {
+      const int t = row / p.G;
+      const int head = g * p.G + row - t * p.G;
+      const float s2 = __ldg(p.sinks + head) * kLog2e;
+      float top = s2;
+#pragma unroll
+      for (int w = 0; w < 8; ++w) top = fmaxf(top, s_m[w][warp]);
+      const float ref = top == -INFINITY ? 0.f : top;
+      float all = s2 == ref ? 1.f : ex2_approx(s2 - ref);
+      float2 z = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < 8; ++w) {
+        const float f = ex2_approx(s_m[w][warp] - ref);
+        const float2 v = *reinterpret_cast<const float2*>(&s_o[w][warp][2 * lane]);
+        all = fmaf(s_l[w][warp], f, all);
+        z.x = fmaf(v.x, f, z.x);
+        z.y = fmaf(v.y, f, z.y);
+      }
+      const float f = all > 0.f ? 1.f / all : 0.f;
+      reinterpret_cast<uint32_t*>(p.out + (static_cast<long long>(rq.t0 + t) * p.Hq + head) * kHeadDim)[lane] =
+          pack_bf16x2(z.x * f, z.y * f);
+      if (lane == 0)
+        p.lse[static_cast<long long>(head) * p.T + rq.t0 + t] = all > 0.f ? (ref + __log2f(all)) * kLn2 : -INFINITY;
+    }
   }
 }
 

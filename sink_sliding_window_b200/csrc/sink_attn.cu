@@ -652,7 +652,9 @@ sink_attn_status check_paged_attn(const sink_attn_paged_dims* d, bool codes) {
   // Positions are 32-bit, with room for a tile behind the last one; so are the
   // blocks of keys of all requests, and a worker's share of them.
   const int64_t tokens = static_cast<int64_t>(d->max_pages) * d->page_size;
-  if (tokens > (int64_t(1) << 30) || tokens * std::max(d->batch, 1) > (int64_t(1) << 35)) return SINK_ATTN_ERR_UNSUPPORTED;
+  const int64_t chunks = (d->num_kv_heads + kRowsHeads - 1) / kRowsHeads;
+  if (tokens > (int64_t(1) << 30) || tokens * std::max(d->batch, 1) > (int64_t(1) << 35) / chunks)
+    return SINK_ATTN_ERR_UNSUPPORTED;
   if (d->q_stride % 8) return SINK_ATTN_ERR_ALIGN;
   return SINK_ATTN_OK;
 }
@@ -688,29 +690,31 @@ struct PagedWorkspace {
 PagedWorkspace paged_workspace(const PagedSplit& s) {
   PagedWorkspace w = {0, 0, 0, 256};
   if (s.rows) {
+    const size_t rows = static_cast<size_t>(kPagedWarps) * 2 * s.kR;
     w.ml = round256(kPagedWarps * sizeof(int4));
-    w.o = w.ml + round256(kPagedWarps * 2 * static_cast<size_t>(s.kR) * sizeof(float2));
-    w.total = w.o + kPagedWarps * 2 * static_cast<size_t>(s.kR) * kHeadDim * sizeof(float);
+    w.o = w.ml + round256(rows * sizeof(float2));
+    w.total = w.o + rows * kHeadDim * sizeof(float);
   }
   return w;
 }
 
-// 4-D view [page][token][head][64] of a paged cache with a box of `tokens`
-// tokens of one head: 128-byte rows (bf16) under the 128-byte swizzle, or
+// 4-D view [page][head][token][64] of a paged cache with a box of `tokens`
+// tokens of `heads` heads: 128-byte rows (bf16) under the 128-byte swizzle, or
 // 64-byte rows (codes) under the 64-byte swizzle.
-bool make_map_paged(CUtensorMap* map, const void* base, const sink_attn_paged_dims* d, bool codes, int tokens) {
+bool make_map_paged(CUtensorMap* map, const void* base, const sink_attn_paged_dims* d, bool codes, int tokens,
+                    int heads) {
   EncodeTiledFn enc = get_encode_tiled();
   if (!enc) return false;
   const cuuint64_t size = codes ? 1 : 2;
-  cuuint64_t dims[4] = {kHeadDim, static_cast<cuuint64_t>(d->num_kv_heads), static_cast<cuuint64_t>(d->page_size),
+  cuuint64_t dims[4] = {kHeadDim, static_cast<cuuint64_t>(d->page_size), static_cast<cuuint64_t>(d->num_kv_heads),
                         static_cast<cuuint64_t>(d->num_pages)};
-  cuuint64_t strides[3] = {static_cast<cuuint64_t>(d->head_stride) * size,
-                           static_cast<cuuint64_t>(d->token_stride) * size,
+  cuuint64_t strides[3] = {static_cast<cuuint64_t>(d->token_stride) * size,
+                           static_cast<cuuint64_t>(d->head_stride) * size,
                            static_cast<cuuint64_t>(d->page_stride) * size};
   // The stride of a dimension of one element is never used, and may be anything.
   for (int i = 0; i < 3; ++i)
     if (dims[i + 1] == 1) strides[i] = kHeadDim * size;
-  cuuint32_t box[4] = {kHeadDim, 1, static_cast<cuuint32_t>(tokens), 1};
+  cuuint32_t box[4] = {kHeadDim, static_cast<cuuint32_t>(tokens), static_cast<cuuint32_t>(heads), 1};
   cuuint32_t estr[4] = {1, 1, 1, 1};
   return enc(map, codes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base),
              dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -733,7 +737,8 @@ bool launch_rows(PagedParams& p, const sink_attn_paged_dims* d, const void* k_ca
   const int box = std::min(d->page_size, kRowsKeys<kF8>);
   p.box_log2 = ilog2_exact(box);
   CUtensorMap tm_k, tm_v;
-  if (!make_map_paged(&tm_k, k_cache, d, kF8, box) || !make_map_paged(&tm_v, v_cache, d, kF8, box)) return false;
+  if (!make_map_paged(&tm_k, k_cache, d, kF8, box, p.per_chunk) ||
+      !make_map_paged(&tm_v, v_cache, d, kF8, box, p.per_chunk)) return false;
   static SmemAttrOnce smem_set;
   if (!smem_set.ensure(sink_attn_paged_rows_kernel<kF8, kR>, rows_smem_bytes(kPagedMaxBatch))) return false;
   const bool join = !rows_never_cut<kF8>(p);
@@ -793,7 +798,7 @@ sink_attn_status paged_attn_impl(const sink_attn_paged_dims* d, const void* q, c
   p.max_pages = d->max_pages;
   p.box_log2 = 0;
   p.few = split.few;
-  p.chunks = (p.Hkv + kRowsWarps - 1) / kRowsWarps;
+  p.chunks = (p.Hkv + kRowsHeads - 1) / kRowsHeads;
   p.per_chunk = (p.Hkv + p.chunks - 1) / p.chunks;
   p.window = window > 0 ? window : 0;
   p.scale_log2 = scale * kLog2e;
