@@ -124,9 +124,11 @@ __device__ __forceinline__ FwdTile fwd_tile(const Geometry& geo, int idx) {
   return w;
 }
 
-// S (64 columns) = Q K^T for the 64 keys whose K rows start at k_addr.
+// S (64 columns) = Q K^T for the 64 keys whose K rows start at k_addr (kF16:
+// both operands are fp16 instead of bf16).
+template <bool kF16 = false>
 __device__ __forceinline__ void fwd_issue_qk(uint32_t tmem_s, uint32_t q_addr, uint32_t k_addr) {
-  constexpr uint32_t idesc = make_idesc_bf16(kBlockM, kHalfN, 0, 0);
+  constexpr uint32_t idesc = kF16 ? make_idesc_f16(kBlockM, kHalfN, 0, 0) : make_idesc_bf16(kBlockM, kHalfN, 0, 0);
 #pragma unroll
   for (int kk = 0; kk < kHeadDim / 16; ++kk) {
     const uint64_t a = make_sdesc_sw128(q_addr + kk * 32, 16, 1024);
@@ -135,10 +137,11 @@ __device__ __forceinline__ void fwd_issue_qk(uint32_t tmem_s, uint32_t q_addr, u
   }
 }
 
-// O += P V for the 64 keys whose V rows start at v_addr; P (bf16 pairs) in
-// the 32 TMEM columns at tmem_p.
+// O += P V for the 64 keys whose V rows start at v_addr; P (bf16 pairs; kF16:
+// fp16) in the 32 TMEM columns at tmem_p.
+template <bool kF16 = false>
 __device__ __forceinline__ void fwd_issue_pv(uint32_t tmem_o, uint32_t tmem_p, uint32_t v_addr, bool accumulate) {
-  constexpr uint32_t idesc = make_idesc_bf16(kBlockM, kHeadDim, 0, 1);
+  constexpr uint32_t idesc = kF16 ? make_idesc_f16(kBlockM, kHeadDim, 0, 1) : make_idesc_bf16(kBlockM, kHeadDim, 0, 1);
 #pragma unroll
   for (int kk = 0; kk < kHalfN / 16; ++kk) {
     const uint64_t b = make_sdesc_sw128(v_addr + kk * 2048, kTileBytes, 1024);
@@ -147,7 +150,7 @@ __device__ __forceinline__ void fwd_issue_pv(uint32_t tmem_o, uint32_t tmem_p, u
 }
 
 // One 64-key step of one query row: mask (kMask), row max, lazily raised
-// reference max, P = 2^(S*scale*log2e - m) packed to bf16 pairs in s[0..31],
+// reference max, P = 2^(S*scale*log2e - m) packed to bf16 (kF16: fp16) pairs in s[0..31],
 // and the row sum of P.  s[] holds the row's 64 fp32 logits on entry.
 struct FwdRowStep {
   bool need;    // the reference max was raised
@@ -156,7 +159,7 @@ struct FwdRowStep {
   float sum;    // sum of this step's P
 };
 
-template <bool kMask>
+template <bool kMask, bool kF16 = false>
 __device__ __forceinline__ FwdRowStep fwd_row_step(uint32_t* s, int c_lo, int c_hi, float sl2, float m_ref) {
   float x[kHalfN];
 #pragma unroll
@@ -188,7 +191,7 @@ __device__ __forceinline__ FwdRowStep fwd_row_step(uint32_t* s, int c_lo, int c_
     const float e1 = ex2_approx(fmaf(x[2 * c + 1], sl2, -m_use));
     acc[(2 * c) & 3] += e0;
     acc[(2 * c + 1) & 3] += e1;
-    s[c] = pack_bf16x2(e0, e1);
+    s[c] = kF16 ? pack_f16x2(e0, e1) : pack_bf16x2(e0, e1);
   }
   r.sum = (acc[0] + acc[1]) + (acc[2] + acc[3]);
   return r;

@@ -1,0 +1,560 @@
+// Paged attention of chunks: requests with more new tokens than the few-rows
+// kernel takes.  Bound by the exponentials and the tensor cores, so it is the
+// two-tile forward (fwd_kernel.cuh) over pages: 128 MMA rows are P = 128 / G
+// tokens of one request times the G heads of a key/value head (any G: the rows
+// behind P * G are idle), a CTA owns a pair of adjacent tiles, and warpgroup b
+// takes the 64-key steps of tile b with S, P and O in tensor memory.
+//
+// Work.  A unit is (request, tile pair, key/value head).  The host knows
+// neither the lengths nor the number of units U; every CTA counts them for
+// itself (one pass over the lengths, a scan, no list in memory) and finds its
+// own, the longer units of a request first.  Two CTAs of a SM make a wave of
+// kChunkWave units.  The units behind the last full wave are cut into k parts
+// along their keys, with k such that the parts fill whole waves as well as
+// they can (chunk_parts): a few rows over a long context take all SMs, and the
+// last wave of 512 units (1.73 waves) is not half empty.  Parts go to the
+// workspace without the sink, and a second kernel joins them.
+//
+// Keys come page by page: a 128-key tile is 2 to 8 TMA boxes of min(page, 64)
+// tokens.  Keys that no row of the request sees (behind its last token, before
+// its window) may hold any bits: their S is masked by selection and their rows
+// of V are zeroed in shared memory by the softmax threads of the steps that
+// hold such keys, since 0 * NaN is not 0.
+//
+// e4m3: the producer warp has the codes of 32 keys at a time copied into a ring
+// of four 2 KB slots and writes them widened to fp16 (exactly) into the same
+// tiles that TMA fills for bf16.  One warp is enough: a tile's 640 instructions
+// and 8 slots fit into the ~2400 cycles that the softmax takes for a tile, and
+// an eleventh warp would leave it 80 registers instead of 96.  Q is converted
+// to fp16 in place (saturating at +-65504) and P rounded to fp16, whose 11 bits
+// reach down to 2^-14 of the row's reference and whose absolute error is 2^-25
+// of it below.  The reference is therefore never the sink.
+#pragma once
+#include "fwd_kernel.cuh"
+#include "paged_attn.cuh"
+
+namespace sa {
+
+constexpr int kChunkWave = 2 * 148;                // CTAs that run at once
+constexpr int kChunkMaxParts = 3 * kChunkWave;     // parts of one call, at most
+constexpr int kChunkFixed = 8;                     // a part's set-up, ends and join, in 64-key steps
+constexpr int kChunkThreads = 320;  // warps 0-7 softmax, 8 MMA, 9 copies (e4m3: and widening)
+constexpr int kChunkMmaWarp = 8;
+constexpr int kChunkSlots = 4;
+constexpr int kChunkSlotKeys = 32;
+constexpr int kChunkSlotBytes = kChunkSlotKeys * kHeadDim;  // e4m3 codes of K or V
+
+struct ChunkParams {
+  PagedParams a;
+  int tokens;          // P: tokens of a query tile
+  float* part_o;       // [part][256 rows][64]
+  float2* part_ml;     // [part][256] (m in log2 units, l)
+  int4* part_unit;     // [cut unit] (request, pair, head, parts)
+  int* part_units;     // cut units of this call
+};
+
+struct ChunkCtl {
+  FwdCtl f;
+  uint64_t q_conv;   // e4m3: Q converted to fp16 in place (256 arrivals)
+  uint64_t codes[kChunkSlots];
+  int units[kChunkThreads / 32];  // sums per warp
+  float steps[kChunkThreads / 32];
+  int unit[2];       // request, unit within it
+};
+
+template <bool kF8>
+constexpr size_t chunk_smem_bytes() {
+  return 1024 + kTileBytes * (2 + 2 * kFwdStages) + (kF8 ? kChunkSlots * kChunkSlotBytes : 0) + sizeof(ChunkCtl);
+}
+
+// Tile pairs of a request, and about how many 64-key steps one of its units has.
+__device__ __forceinline__ int chunk_pairs(const ChunkParams& p, const PagedRequest& r) {
+  return r.n > p.a.few ? (r.n + 2 * p.tokens - 1) / (2 * p.tokens) : 0;
+}
+__device__ __forceinline__ int chunk_steps(const ChunkParams& p, const PagedRequest& r) {
+  const int keys = max(r.len - r.n / 2, 1);
+  return (p.a.window > 0 ? min(keys, p.a.window + 2 * p.tokens) : keys) / kHalfN + 1;
+}
+
+// Parts of each of the `rest` units behind the last full wave, of about
+// `steps` steps each: the k of k = floor(w waves / rest) with the least
+// w (steps / k + fixed).
+__host__ __device__ inline int chunk_parts(int rest, int steps) {
+  int best = 1;
+  float least = static_cast<float>(steps + kChunkFixed);
+  for (int w = 1; rest > 0 && w <= kChunkMaxParts / kChunkWave; ++w) {
+    int k = w * kChunkWave / rest;
+    if (k > steps / kChunkFixed) k = steps / kChunkFixed;
+    if (k < 2) continue;
+    const float cost = w * (static_cast<float>(steps) / k + 2 * kChunkFixed);
+    if (cost < least) least = cost, best = k;
+  }
+  return best;
+}
+
+// Sums over a CTA's threads, in an order that all CTAs share: upto, the units
+// of the threads up to this one, and the totals.
+template <int kWarps>
+__device__ __forceinline__ void chunk_scan(ChunkCtl* cc, int units, float steps, int& upto, int& all_units,
+                                           float& all_steps) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  upto = units;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += v;
+    steps += __shfl_xor_sync(0xffffffffu, steps, o);
+  }
+  if (lane == 31) cc->units[warp] = upto, cc->steps[warp] = steps;
+  __syncthreads();
+  all_units = 0;
+  all_steps = 0.f;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) upto += cc->units[w];
+    all_units += cc->units[w];
+    all_steps += cc->steps[w];
+  }
+}
+
+template <bool kF8>
+__global__ void __launch_bounds__(kChunkThreads, 2)
+    sink_attn_paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                                 const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ ChunkParams p) {
+  constexpr int kThreads = kChunkThreads;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = align1024(smem_raw);
+  uint8_t* sQ = smem;
+  uint8_t* sK = smem + 2 * kTileBytes;
+  uint8_t* sV = sK + kFwdStages * kTileBytes;
+  uint8_t* sB = sV + kFwdStages * kTileBytes;
+  ChunkCtl* cc = reinterpret_cast<ChunkCtl*>(sB + (kF8 ? kChunkSlots * kChunkSlotBytes : 0));
+  FwdCtl* ctl = &cc->f;
+  volatile int* abort = &ctl->abort;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  pdl_launch_dependents();
+
+  // ------------------------------------------------------- which unit, which part
+  int unit, part, parts, slot;
+  PagedRequest rq;
+  int b, pair, g;
+  {
+    const int per = (p.a.batch + kThreads - 1) / kThreads;
+    const int b0 = threadIdx.x * per;
+    int units = 0;
+    float steps = 0.f;
+    for (int i = 0; i < per && b0 + i < p.a.batch; ++i) {
+      if (blockIdx.x == 0) paged_check(p.a, b0 + i);
+      const PagedRequest r = paged_request(p.a, b0 + i);
+      const int n = chunk_pairs(p, r) * p.a.Hkv;
+      units += n;
+      steps += static_cast<float>(n) * chunk_steps(p, r);
+    }
+    int upto, total;
+    float all_steps;
+    chunk_scan<kThreads / 32>(cc, units, steps, upto, total, all_steps);
+    const int full = total / kChunkWave * kChunkWave, rest = total - full;
+    parts = p.part_o && rest ? chunk_parts(rest, static_cast<int>(all_steps / total)) : 1;
+    if (blockIdx.x == 0 && threadIdx.x == 0 && p.part_units) *p.part_units = parts > 1 ? rest : 0;
+    unit = blockIdx.x;
+    part = 0;
+    slot = 0;
+    if (unit >= full) {
+      slot = unit - full;
+      unit = full + slot / parts;
+      part = slot % parts;
+    } else {
+      parts = 1;
+    }
+    if (unit >= total) return;
+    int at = upto - units;
+    if (unit >= at && unit < upto) {
+      for (int i = 0;; ++i) {
+        const int n = chunk_pairs(p, paged_request(p.a, b0 + i)) * p.a.Hkv;
+        if (unit < at + n) {
+          cc->unit[0] = b0 + i;
+          cc->unit[1] = unit - at;
+          break;
+        }
+        at += n;
+      }
+    }
+    if (threadIdx.x == 0) {
+      mbar_init(&ctl->q_full, 1);
+      mbar_init(&cc->q_conv, 2 * kBlockM);
+      for (int s = 0; s < kFwdStages; ++s) {
+        mbar_init(&ctl->k_full[s], 1);
+        mbar_init(&ctl->v_full[s], 1);
+        mbar_init(&ctl->kv_empty[s], 1);
+      }
+      for (int w = 0; w < 2; ++w) {
+        mbar_init(&ctl->s_full[w], 1);
+        mbar_init(&ctl->p_full[w], kBlockM);
+      }
+      mbar_init(&ctl->o_full, 1);
+      for (int s = 0; s < kChunkSlots; ++s) mbar_init(&cc->codes[s], 1);
+      ctl->abort = 0;
+      fence_mbar_init();
+    }
+    if (warp == kChunkMmaWarp) {
+      tmem_alloc(&ctl->tmem_base, kFwdTmemCols);
+      tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    b = cc->unit[0];
+    rq = paged_request(p.a, b);
+    const int at_unit = cc->unit[1];
+    g = at_unit % p.a.Hkv;
+    pair = chunk_pairs(p, rq) - 1 - at_unit / p.a.Hkv;
+  }
+  const uint32_t tmem = ctl->tmem_base;
+  const int G = p.a.G, base = rq.len - rq.n;  // position of the request's first new token
+  const int i0 = pair * 2 * p.tokens;         // the pair's first token within the request
+  const int key_hi = base + min(i0 + 2 * p.tokens, rq.n) - 1;  // the last key any row sees
+  const int box_log2 = p.a.box_log2;
+  const int key_lo = p.a.window > 0 ? max(0, base + i0 - p.a.window + 1) >> box_log2 << box_log2 : 0;
+  // This part's 128-key tiles and 64-key steps.
+  const int halves = key_hi < key_lo ? 1 : (key_hi - key_lo) / kHalfN + 1;
+  const int tiles = (halves + 1) / 2;
+  const int tile0 = static_cast<int>(static_cast<int64_t>(tiles) * part / parts);
+  const int n_tiles = static_cast<int>(static_cast<int64_t>(tiles) * (part + 1) / parts) - tile0;
+  const int n_half = min(halves - 2 * tile0, 2 * n_tiles);
+  const int key0 = key_lo + tile0 * kBlockN;
+
+  if (warp >= kChunkMmaWarp) {
+    if (warp == kChunkMmaWarp) {
+      // ---------------------------------------------------------- MMA issuer
+      // As in the two-tile forward: S_b(h) -> P_b(h) -> O_b += P_b V(h) ->
+      // S_b(h+1) into the buffer that P_b(h) just left.
+      if (n_half > 0 && elect_one()) {
+        mbar_arrive_expect_tx(&ctl->q_full, 2 * p.tokens * G * kHeadDim * 2);
+        for (int u = 0; u < 2; ++u)
+          tma_load_3d(sQ + u * kTileBytes, &tm_q, &ctl->q_full, 0, g * G, rq.t0 + i0 + u * p.tokens);
+        const uint32_t tS = tmem + kFwdTmemS;
+        const uint32_t tO = tmem + kFwdTmemO;
+        bool ok = mbar_wait(kF8 ? &cc->q_conv : &ctl->q_full, 0, abort, &g_device_error, kDevErrTimeoutMma) &&
+                  mbar_wait(&ctl->k_full[0], 0, abort, &g_device_error, kDevErrTimeoutMma);
+        if (ok) {
+          tc_fence_after();
+#pragma unroll
+          for (int w = 0; w < 2; ++w) {
+            fwd_issue_qk<kF8>(tS + w * kHalfN, smem_u32(sQ + w * kTileBytes), smem_u32(sK));
+            tc_commit(&ctl->s_full[w]);
+          }
+        }
+        for (int h = 0; ok && h < n_half; ++h) {
+          const int j = h >> 1, s = j % kFwdStages;
+          const int hn = h + 1, jn = hn >> 1, sn = jn % kFwdStages;
+          ok = mbar_wait(&ctl->v_full[s], (j / kFwdStages) & 1, abort, &g_device_error, kDevErrTimeoutMma) &&
+               (hn >= n_half ||
+                mbar_wait(&ctl->k_full[sn], (jn / kFwdStages) & 1, abort, &g_device_error, kDevErrTimeoutMma));
+          for (int w = 0; ok && w < 2; ++w) {
+            ok = mbar_wait(&ctl->p_full[w], h & 1, abort, &g_device_error, kDevErrTimeoutMma);
+            if (!ok) break;
+            tc_fence_after();
+            fwd_issue_pv<kF8>(tO + w * kHeadDim, tS + w * kHalfN, smem_u32(sV + s * kTileBytes) + (h & 1) * kHalfBytes,
+                              h > 0);
+            if (hn < n_half) {
+              fwd_issue_qk<kF8>(tS + w * kHalfN, smem_u32(sQ + w * kTileBytes),
+                                smem_u32(sK + sn * kTileBytes) + (hn & 1) * kHalfBytes);
+              tc_commit(&ctl->s_full[w]);
+            }
+          }
+          if (ok && ((h & 1) == 1 || h == n_half - 1)) tc_commit(&ctl->kv_empty[s]);
+        }
+        if (ok) tc_commit(&ctl->o_full);
+      }
+    } else if constexpr (!kF8) {
+      // ---------------------------------------------------------- TMA producer
+      // Lane x looks up the page of box x, a tile ahead of the copies.
+      const int nbox = kBlockN >> box_log2, page_mask = (1 << p.a.page_log2) - 1;
+      auto wanted = [&](int j) { return lane < nbox && key0 + j * kBlockN + (lane << box_log2) <= key_hi; };
+      auto entry = [&](int j) { return paged_entry(p.a, b, key0 + j * kBlockN + (lane << box_log2)); };
+      int next = wanted(0) ? entry(0) : 0;
+      bool ok = true;
+      for (int j = 0; ok && j < n_tiles; ++j) {
+        const int s = j % kFwdStages;
+        const int mine = wanted(j) ? paged_page(p.a, next) : p.a.num_pages;
+        if (j + 1 < n_tiles && wanted(j + 1)) next = entry(j + 1);
+        if (j >= kFwdStages)
+          ok = warp_all(mbar_wait(&ctl->kv_empty[s], ((j / kFwdStages) - 1) & 1, abort, &g_device_error,
+                                  kDevErrTimeoutProducer));
+        if (!ok) break;
+        if (elect_one()) {
+          mbar_arrive_expect_tx(&ctl->k_full[s], kTileBytes);
+          mbar_arrive_expect_tx(&ctl->v_full[s], kTileBytes);
+        }
+        __syncwarp();
+        for (int x = 0; x < nbox; ++x) {
+          const int page = __shfl_sync(0xffffffffu, mine, x);
+          const int at = (key0 + j * kBlockN + (x << box_log2)) & page_mask;
+          if (elect_one()) {
+            const int to = s * kTileBytes + (x << box_log2) * kHeadDim * 2;
+            tma_load_4d(sK + to, &tm_k, &ctl->k_full[s], 0, at, g, page);
+            tma_load_4d(sV + to, &tm_v, &ctl->v_full[s], 0, at, g, page);
+          }
+          __syncwarp();
+        }
+      }
+    } else {
+      // -------------------------------------------------- e4m3: copy and widen
+      // Slot q holds 32 keys: of tile q / 8 those of K, four slots, then those
+      // of V.  Rows that no row of the request sees become zeros.
+      const int nbox = kBlockN >> box_log2, page_mask = (1 << p.a.page_log2) - 1;
+      const int per_slot = kChunkSlotKeys >> box_log2;
+      auto wanted = [&](int j) { return lane < nbox && key0 + j * kBlockN + (lane << box_log2) <= key_hi; };
+      auto entry = [&](int j) { return paged_entry(p.a, b, key0 + j * kBlockN + (lane << box_log2)); };
+      int next = wanted(0) ? entry(0) : 0, mine = 0;
+      const int slots = 8 * n_tiles;
+      int issued = 0;
+      auto fetch = [&]() {  // by the whole warp
+        const int j = issued >> 3, e = issued & 7;
+        if (e == 0) {
+          mine = wanted(j) ? paged_page(p.a, next) : p.a.num_pages;
+          if (j + 1 < n_tiles && wanted(j + 1)) next = entry(j + 1);
+        }
+        uint64_t* full = &cc->codes[issued % kChunkSlots];
+        uint8_t* to = sB + issued % kChunkSlots * kChunkSlotBytes;
+        if (elect_one()) mbar_arrive_expect_tx(full, kChunkSlotBytes);
+        __syncwarp();
+        for (int x = 0; x < per_slot; ++x) {
+          const int box = (e & 3) * per_slot + x;
+          const int page = __shfl_sync(0xffffffffu, mine, box);
+          const int at = (key0 + j * kBlockN + (box << box_log2)) & page_mask;
+          if (elect_one())
+            tma_load_4d(to + (x << box_log2) * kHeadDim, e < 4 ? &tm_k : &tm_v, full, 0, at, g, page);
+          __syncwarp();
+        }
+        ++issued;
+      };
+      while (issued < min(kChunkSlots, slots)) fetch();
+      bool ok = true;
+      int q = 0;
+      for (; q < slots; ++q) {
+        const int j = q >> 3, e = q & 7, s = j % kFwdStages, slot_q = q % kChunkSlots;
+        if (e == 0 && j >= kFwdStages)
+          ok = warp_all(mbar_wait(&ctl->kv_empty[s], ((j / kFwdStages) - 1) & 1, abort, &g_device_error,
+                                  kDevErrTimeoutProducer));
+        ok = ok && warp_all(mbar_wait(&cc->codes[slot_q], (q / kChunkSlots) & 1, abort, &g_device_error,
+                                      kDevErrTimeoutProducer));
+        if (!ok) break;
+        uint4 v[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {  // 16 codes: row lane / 4 + 8 u, 16-byte piece lane % 4
+          const int row = (lane >> 2) + 8 * u;
+          v[u] = *reinterpret_cast<const uint4*>(sB + slot_q * kChunkSlotBytes + row * kHeadDim +
+                                                 (((lane & 3) ^ ((row >> 1) & 3)) << 4));
+        }
+        uint8_t* tile = (e < 4 ? sK : sV) + s * kTileBytes + (e & 3) * kChunkSlotKeys * 128;
+        const int key = key0 + j * kBlockN + (e & 3) * kChunkSlotKeys + (lane >> 2);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int row = (lane >> 2) + 8 * u;
+          if (key + 8 * u < rq.lo || key + 8 * u >= rq.len) v[u] = make_uint4(0u, 0u, 0u, 0u);
+          const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+            *reinterpret_cast<uint4*>(tile + row * 128 + (((2 * (lane & 3) + c) ^ (row & 7)) << 4)) =
+                make_uint4(e4m3x2_to_f16x2(w[2 * c]), e4m3x2_to_f16x2(w[2 * c] >> 16), e4m3x2_to_f16x2(w[2 * c + 1]),
+                           e4m3x2_to_f16x2(w[2 * c + 1] >> 16));
+        }
+        fence_proxy_async_smem();  // the tile for the MMA; the slot's reads before its next copy
+        __syncwarp();
+        if ((e & 3) == 3 && lane == 0) mbar_arrive(e < 4 ? &ctl->k_full[s] : &ctl->v_full[s]);
+        if (issued < slots) fetch();
+      }
+      if (!ok) {
+        // Copies in flight still write to this CTA's shared memory.
+        for (; q < issued; ++q) {
+          const uint64_t t0 = global_timer_ns();
+          while (!mbar_try_wait(&cc->codes[q % kChunkSlots], (q / kChunkSlots) & 1) &&
+                 global_timer_ns() - t0 < kWaitLimitNs / 4) {
+          }
+        }
+      }
+    }
+  } else {
+    // --------------------------------------------- softmax (1 row per thread)
+    const int wg = warp >> 2;
+    const int r = threadIdx.x & (kBlockM - 1);
+    const int row_t = r / G;
+    const int it = i0 + wg * p.tokens + row_t;  // token within the request
+    const bool valid = row_t < p.tokens && it < rq.n;
+    const int h = g * G + r - row_t * G;
+    // Allowed keys [lo_r, hi_r] of this row; empty for idle rows.
+    const int hi_r = valid ? base + it : -1;
+    const int lo_r = valid && p.a.window > 0 ? max(0, hi_r - p.a.window + 1) : 0;
+    // Keys that every row of this warpgroup's tile sees: [all_lo, all_hi].
+    const int w0 = i0 + wg * p.tokens, w1 = min(w0 + p.tokens, rq.n) - 1;
+    const int all_hi = w0 <= w1 ? base + w0 : -1;
+    const int all_lo = p.a.window > 0 ? max(0, base + w1 - p.a.window + 1) : 0;
+    float m_ref = -INFINITY, l = 0.f;
+    const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + lane_base + kFwdTmemS + wg * kHalfN;
+    const uint32_t tO = tmem + lane_base + kFwdTmemO + wg * kHeadDim;
+    const float sl2 = kF8 ? p.a.scale_log2 * __ldg(p.a.k_scale + g) : p.a.scale_log2;
+    bool ok = n_half > 0;  // a part of a unit with fewer tiles than parts may have none
+    if constexpr (kF8) {
+      ok = ok && warp_all(mbar_wait(&ctl->q_full, 0, abort, &g_device_error, kDevErrTimeoutSoftmax));
+      if (ok) {
+        // Rows of 128 bytes, so elementwise in place whatever the swizzle.
+        uint32_t* row = reinterpret_cast<uint32_t*>(sQ + wg * kTileBytes + r * 128);
+#pragma unroll 8
+        for (int c = 0; c < 32; ++c) {
+          const int at = (c + r) & 31;  // 32 lanes, 32 banks
+          row[at] = bf16x2_to_f16x2_sat(row[at]);
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(&cc->q_conv);
+      }
+    }
+
+    for (int hs = 0; ok && hs < n_half; ++hs) {
+      ok = warp_all(mbar_wait(&ctl->s_full[wg], hs & 1, abort, &g_device_error, kDevErrTimeoutSoftmax));
+      if (!ok) break;
+      tc_fence_after();
+      uint32_t sr[kHalfN];
+      tmem_ld64(tS, sr);
+      const int ks = key0 + hs * kHalfN;
+      FwdRowStep st;
+      if (ks + kHalfN - 1 > all_hi || ks < all_lo)
+        st = fwd_row_step<true, kF8>(sr, lo_r - ks, hi_r - ks, sl2, m_ref);
+      else
+        st = fwd_row_step<false, kF8>(sr, 0, 0, sl2, m_ref);
+      l = l * st.alpha + st.sum;
+      __syncwarp();
+      tmem_st32(tS, sr);
+      if (hs > 0 && __any_sync(0xffffffffu, st.need)) {
+        uint32_t o[kHeadDim];
+        tmem_ld64(tO, o);
+#pragma unroll
+        for (int c = 0; c < kHeadDim; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * st.alpha);
+        tmem_st32(tO, o);
+        tmem_st32(tO + 32, o + 32);
+      }
+      m_ref = st.m_new;
+      if constexpr (!kF8) {
+        // Keys of the step that no row of the request sees: zero rows of V.
+        // Both warpgroups write them, each before its own PV.
+        if (ks < rq.lo || ks + kHalfN > rq.len) {
+          const int j = hs >> 1, s = j % kFwdStages;
+          ok = warp_all(mbar_wait(&ctl->v_full[s], (j / kFwdStages) & 1, abort, &g_device_error, kDevErrTimeoutSoftmax));
+          if (!ok) break;
+          const int key = ks + (r >> 1);
+          if (key < rq.lo || key >= rq.len) {
+            uint4* row = reinterpret_cast<uint4*>(sV + s * kTileBytes + ((hs & 1) * kHalfN + (r >> 1)) * 128 + (r & 1) * 64);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) row[c] = make_uint4(0u, 0u, 0u, 0u);
+          }
+          fence_proxy_async_smem();
+        }
+      }
+      tc_fence_before();
+      mbar_arrive(&ctl->p_full[wg]);
+    }
+
+    // ---------------------------------------------------------------- epilogue
+    if (n_half == 0) {
+      p.part_ml[static_cast<long long>(slot) * 2 * kBlockM + wg * kBlockM + r] = make_float2(-INFINITY, 0.f);
+      if (part == 0 && threadIdx.x == 0) p.part_unit[slot / parts] = make_int4(b, pair, g, parts);
+    }
+    if (ok) ok = mbar_wait(&ctl->o_full, 0, abort, &g_device_error, kDevErrTimeoutEpilogue);
+    ok = warp_all(ok);
+    if (ok) {
+      tc_fence_after();
+      uint32_t o[kHeadDim];
+      __syncwarp();
+      tmem_ld64(tO, o);
+      const float vs = kF8 ? __ldg(p.a.v_scale + g) : 1.f;
+      if (parts > 1) {
+        const long long at = static_cast<long long>(slot) * 2 * kBlockM + wg * kBlockM + r;
+        p.part_ml[at] = make_float2(m_ref, l);
+        if (part == 0 && threadIdx.x == 0) p.part_unit[slot / parts] = make_int4(b, pair, g, parts);
+        float4* dst = reinterpret_cast<float4*>(p.part_o + at * kHeadDim);
+        if (valid) {
+#pragma unroll
+          for (int c = 0; c < kHeadDim / 4; ++c)
+            dst[c] = make_float4(__uint_as_float(o[4 * c]) * vs, __uint_as_float(o[4 * c + 1]) * vs,
+                                 __uint_as_float(o[4 * c + 2]) * vs, __uint_as_float(o[4 * c + 3]) * vs);
+        }
+      } else if (valid) {
+        const float s2 = __ldg(p.a.sinks + h) * kLog2e;
+        const float top = fmaxf(s2, m_ref);
+        float f = 0.f, all = 0.f;
+        if (top != -INFINITY) {
+          f = ex2_approx(m_ref - top);
+          all = fmaf(l, f, s2 == top ? 1.f : ex2_approx(s2 - top));
+        }
+        f = all > 0.f ? vs * f / all : 0.f;
+        const int t = rq.t0 + it;
+        uint4* dst = reinterpret_cast<uint4*>(p.a.out + (static_cast<long long>(t) * p.a.Hq + h) * kHeadDim);
+#pragma unroll
+        for (int c = 0; c < kHeadDim / 8; ++c) {
+          uint4 v;
+          v.x = pack_bf16x2(__uint_as_float(o[8 * c + 0]) * f, __uint_as_float(o[8 * c + 1]) * f);
+          v.y = pack_bf16x2(__uint_as_float(o[8 * c + 2]) * f, __uint_as_float(o[8 * c + 3]) * f);
+          v.z = pack_bf16x2(__uint_as_float(o[8 * c + 4]) * f, __uint_as_float(o[8 * c + 5]) * f);
+          v.w = pack_bf16x2(__uint_as_float(o[8 * c + 6]) * f, __uint_as_float(o[8 * c + 7]) * f);
+          dst[c] = v;
+        }
+        p.a.lse[static_cast<long long>(h) * p.a.T + t] = all > 0.f ? (top + __log2f(all)) * kLn2 : -INFINITY;
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kChunkMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kFwdTmemCols);
+  }
+}
+
+// Joins the parts of the cut units and adds the sink.  One CTA per cut unit
+// and 32 of its 256 rows; half a warp per row, four dims per lane.
+__global__ void __launch_bounds__(256) sink_attn_paged_chunk_join_kernel(const __grid_constant__ ChunkParams p) {
+  pdl_wait();
+  const int i = blockIdx.x;
+  if (i >= __ldcg(p.part_units)) return;
+  const int4 u = __ldcg(p.part_unit + i);
+  const PagedRequest rq = paged_request(p.a, u.x);
+  const int d = threadIdx.x & 15;
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    const int row = blockIdx.y * 32 + x * 16 + (threadIdx.x >> 4);
+    const int r = row & (kBlockM - 1), row_t = r / p.a.G;
+    const int it = (2 * u.y + (row >> 7)) * p.tokens + row_t;
+    if (row_t >= p.tokens || it >= rq.n) continue;
+    const int h = u.z * p.a.G + r - row_t * p.a.G;
+    const float s2 = __ldg(p.a.sinks + h) * kLog2e;
+    float m = -INFINITY, l = 0.f;
+    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int k = 0; k < u.w; ++k) {
+      const long long at = (static_cast<long long>(i) * u.w + k) * 2 * kBlockM + row;
+      const float2 ml = __ldcg(p.part_ml + at);
+      const float4 v = __ldcg(reinterpret_cast<const float4*>(p.part_o + at * kHeadDim) + d);
+      const float now = fmaxf(m, ml.x);
+      if (ml.x == -INFINITY) continue;  // a part of no keys, or of none that the row sees
+      const float f0 = ex2_approx(m - now), f1 = ex2_approx(ml.x - now);
+      m = now;
+      l = l * f0 + ml.y * f1;
+      y = make_float4(y.x * f0 + v.x * f1, y.y * f0 + v.y * f1, y.z * f0 + v.z * f1, y.w * f0 + v.w * f1);
+    }
+    const float top = fmaxf(m, s2);
+    float f = 0.f, all = 0.f;
+    if (top != -INFINITY) {
+      f = ex2_approx(m - top);
+      all = fmaf(l, f, s2 == top ? 1.f : ex2_approx(s2 - top));
+    }
+    f = all > 0.f ? f / all : 0.f;
+    const int t = rq.t0 + it;
+    *reinterpret_cast<uint2*>(p.a.out + (static_cast<long long>(t) * p.a.Hq + h) * kHeadDim + 4 * d) =
+        make_uint2(pack_bf16x2(y.x * f, y.y * f), pack_bf16x2(y.z * f, y.w * f));
+    if (d == 0) p.a.lse[static_cast<long long>(h) * p.a.T + t] = all > 0.f ? (top + __log2f(all)) * kLn2 : -INFINITY;
+  }
+}
+
+}  // namespace sa

@@ -22,7 +22,7 @@
 #include "paged_append.cuh"
 #include "paged_attn.cuh"
 #include "paged_rows.cuh"
-#include "paged_long.cuh"
+#include "paged_chunk.cuh"
 
 namespace sa {
 namespace {
@@ -682,19 +682,53 @@ PagedSplit split_paged(const sink_attn_paged_dims* d) {
 constexpr int kPagedCtas = 148;  // one CTA per SM of a B200
 constexpr int kPagedWarps = kPagedCtas * kRowsWarps;
 
-// Workspace of a call (bytes): the pieces of cut units.
-struct PagedWorkspace {
-  size_t unit, ml, o, total;
+// Upper bound of the chunk kernel's units, and of the parts its last units are
+// cut into (0: their keys are too few to be cut).  The lengths are not known here.
+struct ChunkBound {
+  int64_t units, parts;
 };
 
-PagedWorkspace paged_workspace(const PagedSplit& s) {
-  PagedWorkspace w = {0, 0, 0, 256};
+ChunkBound chunk_bound(const sink_attn_paged_dims* d, const PagedSplit& s, int window) {
+  ChunkBound c;
+  const int tokens = kBlockM / (d->num_q_heads / d->num_kv_heads);
+  const int64_t requests = std::min<int64_t>(d->batch, d->total_tokens / (s.few + 1));
+  c.units = d->num_kv_heads * (d->total_tokens / (2 * tokens) + requests);
+  const int64_t keys = std::min<int64_t>(int64_t(d->max_pages) * d->page_size,
+                                         window > 0 ? int64_t(window) + 2 * tokens : INT64_MAX);
+  const int64_t most = (keys / kHalfN + 1) / kChunkFixed;  // parts of a unit
+  c.parts = most < 2 ? 0 : std::min<int64_t>(kChunkMaxParts, std::min<int64_t>(c.units, kChunkWave) * most);
+  return c;
+}
+
+// Workspace of a call (bytes): the pieces of cut units of both kernels.
+struct PagedWorkspace {
+  size_t unit, ml, o;
+  size_t chunk_units, chunk_unit, chunk_ml, chunk_o;
+  size_t total;
+};
+
+PagedWorkspace paged_workspace(const sink_attn_paged_dims* d, const PagedSplit& s) {
+  PagedWorkspace w = {};
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t here = at;
+    at += round256(bytes);
+    return here;
+  };
   if (s.rows) {
     const size_t rows = static_cast<size_t>(kPagedWarps) * 2 * s.kR;
-    w.ml = round256(kPagedWarps * sizeof(int4));
-    w.o = w.ml + round256(rows * sizeof(float2));
-    w.total = w.o + rows * kHeadDim * sizeof(float);
+    w.unit = take(kPagedWarps * sizeof(int4));
+    w.ml = take(rows * sizeof(float2));
+    w.o = take(rows * kHeadDim * sizeof(float));
   }
+  if (s.chunks) {
+    const size_t rows = static_cast<size_t>(chunk_bound(d, s, 0).parts) * 2 * kBlockM;
+    w.chunk_units = take(sizeof(int));
+    w.chunk_unit = take(kChunkWave * sizeof(int4));
+    w.chunk_ml = take(rows * sizeof(float2));
+    w.chunk_o = take(rows * kHeadDim * sizeof(float));
+  }
+  w.total = std::max<size_t>(at, 256);
   return w;
 }
 
@@ -731,6 +765,21 @@ bool rows_never_cut(const PagedParams& p) {
   return (keys + lead + kRowsKeys<kF8> - 1) / kRowsKeys<kF8> <= 2 * kRowsSnap<kF8> + 1;
 }
 
+// Launches a 256-thread kernel that waits by itself for the kernel before it.
+template <typename P>
+bool launch_join(void (*kernel)(P), dim3 grid, const P& p, cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(256, 1, 1);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess;
+}
+
 template <bool kF8, int kR>
 bool launch_rows(PagedParams& p, const sink_attn_paged_dims* d, const void* k_cache, const void* v_cache,
                  cudaStream_t st) {
@@ -746,16 +795,7 @@ bool launch_rows(PagedParams& p, const sink_attn_paged_dims* d, const void* k_ca
   sink_attn_paged_rows_kernel<kF8, kR><<<kPagedCtas, kRowsThreads, rows_smem_bytes(p.batch), st>>>(tm_k, tm_v, p);
   if (cudaPeekAtLastError() != cudaSuccess) return false;
   if (!join) return true;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(kPagedCtas * (kRowsWarps / p.per_chunk), p.per_chunk, 1);
-  cfg.blockDim = dim3(256, 1, 1);
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, sink_attn_paged_join_kernel<kR>, p) == cudaSuccess;
+  return launch_join(sink_attn_paged_join_kernel<kR>, dim3(kPagedCtas * (kRowsWarps / p.per_chunk), p.per_chunk), p, st);
 }
 
 template <bool kF8>
@@ -764,6 +804,40 @@ bool launch_rows(int kR, PagedParams& p, const sink_attn_paged_dims* d, const vo
   return kR == 8    ? launch_rows<kF8, 8>(p, d, k_cache, v_cache, st)
          : kR == 16 ? launch_rows<kF8, 16>(p, d, k_cache, v_cache, st)
                     : launch_rows<kF8, 32>(p, d, k_cache, v_cache, st);
+}
+
+// The query tile of the chunk kernel, `tokens` tokens of one group of heads.
+bool make_map_paged_q(CUtensorMap* map, const sink_attn_paged_dims* d, const void* q, int G, int tokens) {
+  EncodeTiledFn enc = get_encode_tiled();
+  if (!enc) return false;
+  cuuint64_t dims[3] = {kHeadDim, static_cast<cuuint64_t>(d->num_q_heads), static_cast<cuuint64_t>(d->total_tokens)};
+  cuuint64_t strides[2] = {kHeadDim * 2, static_cast<cuuint64_t>(d->q_stride) * 2};
+  if (dims[2] == 1) strides[1] = dims[1] * strides[0];
+  cuuint32_t box[3] = {kHeadDim, static_cast<cuuint32_t>(G), static_cast<cuuint32_t>(tokens)};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(q), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <bool kF8>
+bool launch_chunks(ChunkParams& p, const sink_attn_paged_dims* d, const void* k_cache, const void* v_cache,
+                   const ChunkBound& bound, cudaStream_t st) {
+  CUtensorMap tm_q, tm_k, tm_v;
+  const int box = std::min(d->page_size, kF8 ? kChunkSlotKeys : kHalfN);
+  p.a.box_log2 = ilog2_exact(box);
+  if (!make_map_paged_q(&tm_q, d, p.a.q, p.a.G, p.tokens) || !make_map_paged(&tm_k, k_cache, d, kF8, box, 1) ||
+      !make_map_paged(&tm_v, v_cache, d, kF8, box, 1))
+    return false;
+  static SmemAttrOnce smem_set;
+  if (!smem_set.ensure(sink_attn_paged_chunk_kernel<kF8>, chunk_smem_bytes<kF8>())) return false;
+  if (bound.parts == 0) p.part_o = nullptr;
+  sink_attn_paged_chunk_kernel<kF8><<<static_cast<unsigned>(bound.units + bound.parts), kChunkThreads,
+                                      chunk_smem_bytes<kF8>(), st>>>(tm_q, tm_k, tm_v, p);
+  if (cudaPeekAtLastError() != cudaSuccess) return false;
+  if (bound.parts == 0) return true;
+  const unsigned cut = static_cast<unsigned>(std::min<int64_t>(bound.units, kChunkWave - 1));
+  return launch_join(sink_attn_paged_chunk_join_kernel, dim3(cut, 2 * kBlockM / 32), p, st);
 }
 
 sink_attn_status paged_attn_impl(const sink_attn_paged_dims* d, const void* q, const void* k_cache,
@@ -783,7 +857,7 @@ sink_attn_status paged_attn_impl(const sink_attn_paged_dims* d, const void* q, c
       !aligned4(v_scale))
     return SINK_ATTN_ERR_ALIGN;
   const PagedSplit split = split_paged(d);
-  const PagedWorkspace ws = paged_workspace(split);
+  const PagedWorkspace ws = paged_workspace(d, split);
   if (workspace_bytes < ws.total || !workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u))
     return SINK_ATTN_ERR_WORKSPACE;
   PagedParams p;
@@ -817,17 +891,24 @@ sink_attn_status paged_attn_impl(const sink_attn_paged_dims* d, const void* q, c
   p.part_ml = reinterpret_cast<float2*>(base + ws.ml);
   p.part_o = reinterpret_cast<float*>(base + ws.o);
   cudaStream_t st_ = static_cast<cudaStream_t>(stream);
+  if (split.chunks) {
+    ChunkParams c;
+    c.a = p;
+    c.tokens = kBlockM / p.G;
+    c.part_units = reinterpret_cast<int*>(base + ws.chunk_units);
+    c.part_unit = reinterpret_cast<int4*>(base + ws.chunk_unit);
+    c.part_ml = reinterpret_cast<float2*>(base + ws.chunk_ml);
+    c.part_o = reinterpret_cast<float*>(base + ws.chunk_o);
+    const ChunkBound bound = chunk_bound(d, split, p.window);
+    if (bound.units + bound.parts > 0x7fffffff) return SINK_ATTN_ERR_UNSUPPORTED;
+    if (!(codes ? launch_chunks<true>(c, d, k_cache, v_cache, bound, st_)
+                : launch_chunks<false>(c, d, k_cache, v_cache, bound, st_)))
+      return SINK_ATTN_ERR_CUDA;
+  }
   if (split.rows && !(codes ? launch_rows<true>(split.kR, p, d, k_cache, v_cache, st_)
                             : launch_rows<false>(split.kR, p, d, k_cache, v_cache, st_)))
     return SINK_ATTN_ERR_CUDA;
-  if (split.chunks) {
-    const long long rows = static_cast<long long>(p.T) * p.G;
-    if ((rows + 127) / 128 > 0x7fffffff || p.Hkv > 65535) return SINK_ATTN_ERR_UNSUPPORTED;
-    const dim3 grid(static_cast<unsigned>((rows + 127) / 128), static_cast<unsigned>(p.Hkv));
-    if (codes) sink_attn_paged_kernel<true><<<grid, 128, 0, st_>>>(p, k_cache, v_cache, d->page_stride, d->token_stride, d->head_stride);
-    else sink_attn_paged_kernel<false><<<grid, 128, 0, st_>>>(p, k_cache, v_cache, d->page_stride, d->token_stride, d->head_stride);
-  }
-  return cudaPeekAtLastError() == cudaSuccess ? SINK_ATTN_OK : SINK_ATTN_ERR_CUDA;
+  return SINK_ATTN_OK;
 }
 
 }  // namespace
@@ -913,7 +994,7 @@ sink_attn_status sink_attn_paged_append_e4m3(const sink_attn_paged_dims* d, cons
 }
 
 size_t sink_attn_paged_workspace_size(const sink_attn_paged_dims* d) {
-  return check_paged_attn(d, false) == SINK_ATTN_OK ? paged_workspace(split_paged(d)).total : 0;
+  return check_paged_attn(d, false) == SINK_ATTN_OK ? paged_workspace(d, split_paged(d)).total : 0;
 }
 
 sink_attn_status sink_attn_paged_attn(const sink_attn_paged_dims* d, const void* q, const void* k_cache,
