@@ -2,18 +2,18 @@
 // kernel takes.  Bound by the exponentials and the tensor cores, so it is the
 // two-tile forward (fwd_kernel.cuh) over pages: 128 MMA rows are P = 128 / G
 // tokens of one request times the G heads of a key/value head (any G: the rows
-// behind P * G are idle), a CTA owns a pair of adjacent tiles, and warpgroup b
+// behind P * G are idle), a CTA owns kTiles adjacent tiles, and warpgroup b
 // takes the 64-key steps of tile b with S, P and O in tensor memory.
 //
-// Work.  A unit is (request, tile pair, key/value head).  The host knows
+// Work.  A unit is (request, kTiles tiles, key/value head).  The host knows
 // neither the lengths nor the number of units U; every CTA counts them for
 // itself (one pass over the lengths, a scan, no list in memory) and finds its
-// own, the longer units of a request first.  Two CTAs of a SM make a wave of
-// kChunkWave units.  The units behind the last full wave are cut into k parts
-// along their keys, with k such that the parts fill whole waves as well as
-// they can (chunk_parts): a few rows over a long context take all SMs, and the
-// last wave of 512 units (1.73 waves) is not half empty.  Parts go to the
-// workspace without the sink, and a second kernel joins them.
+// own, the longer units of a request first.  The CTAs that run at once make a
+// wave.  The units behind the last full wave are cut into k parts along their
+// keys, with k such that the parts fill whole waves as well as they can
+// (chunk_parts): a few rows over a long context take all SMs, and the last
+// wave of 512 units (1.73 waves) is not half empty.  Parts go to the workspace
+// without the sink, and a second kernel joins them.
 //
 // Keys come page by page: a 128-key tile is 2 to 8 TMA boxes of min(page, 64)
 // tokens.  Keys that no row of the request sees (behind its last token, before
@@ -21,70 +21,91 @@
 // of V are zeroed in shared memory by the softmax threads of the steps that
 // hold such keys, since 0 * NaN is not 0.
 //
-// e4m3: the producer warp has the codes of 32 keys at a time copied into a ring
-// of four 2 KB slots and writes them widened to fp16 (exactly) into the same
-// tiles that TMA fills for bf16.  One warp is enough: a tile's 640 instructions
-// and 8 slots fit into the ~2400 cycles that the softmax takes for a tile, and
-// an eleventh warp would leave it 80 registers instead of 96.  Q is converted
-// to fp16 in place (saturating at +-65504) and P rounded to fp16, whose 11 bits
-// reach down to 2^-14 of the row's reference and whose absolute error is 2^-25
-// of it below.  The reference is therefore never the sink.
+// e4m3: the codes come by TMA into a ring of 2 KB slots, and two warps write
+// them widened to fp16 (exactly) into the same tiles that TMA fills for bf16.
+// Widening costs as much for two query tiles as for four, so one CTA of four
+// tiles and twenty warps takes the place of two CTAs of two tiles and ten
+// warps each: with the latter, whose registers leave room for one warp to copy
+// and widen, that warp took 3 us for a 64-key step.  Q is converted to fp16 in
+// place (saturating at +-65504) and P rounded to fp16, whose 11 bits reach down
+// to 2^-14 of the row's reference and whose absolute error is 2^-25 of it
+// below.  The reference is therefore never the sink.
 #pragma once
 #include "fwd_kernel.cuh"
 #include "paged_attn.cuh"
 
 namespace sa {
 
-constexpr int kChunkWave = 2 * 148;                // CTAs that run at once
-constexpr int kChunkMaxParts = 3 * kChunkWave;     // parts of one call, at most
-constexpr int kChunkFixed = 8;                     // a part's set-up, ends and join, in 64-key steps
-constexpr int kChunkThreads = 320;  // warps 0-7 softmax, 8 MMA, 9 copies (e4m3: and widening)
-constexpr int kChunkMmaWarp = 8;
-constexpr int kChunkSlots = 4;
+// Query tiles of a CTA, its warps (softmax warpgroups first, then MMA, copies
+// and, for e4m3, two that widen) and CTAs of a SM.
+template <bool kF8>
+constexpr int kChunkTiles = kF8 ? 4 : 2;
+template <bool kF8>
+constexpr int kChunkThreads = kF8 ? 640 : 320;
+template <bool kF8>
+constexpr int kChunkPerSm = kF8 ? 1 : 2;
+constexpr int kChunkSms = 148;
+constexpr int kChunkMaxWaves = 3;  // of parts
+constexpr int kChunkFixed = 8;     // a part's set-up, ends and join, in 64-key steps
+constexpr int kChunkSlots = 8;
 constexpr int kChunkSlotKeys = 32;
 constexpr int kChunkSlotBytes = kChunkSlotKeys * kHeadDim;  // e4m3 codes of K or V
 
 struct ChunkParams {
   PagedParams a;
   int tokens;          // P: tokens of a query tile
-  float* part_o;       // [part][256 rows][64]
-  float2* part_ml;     // [part][256] (m in log2 units, l)
-  int4* part_unit;     // [cut unit] (request, pair, head, parts)
+  int wave;            // CTAs that run at once
+  float* part_o;       // [part][kTiles * 128 rows][64]
+  float2* part_ml;     // [part][kTiles * 128] (m in log2 units, l)
+  int4* part_unit;     // [cut unit] (request, unit within its head, head, parts)
   int* part_units;     // cut units of this call
 };
 
+template <bool kF8>
 struct ChunkCtl {
-  FwdCtl f;
-  uint64_t q_conv;   // e4m3: Q converted to fp16 in place (256 arrivals)
-  uint64_t codes[kChunkSlots];
-  int units[kChunkThreads / 32];  // sums per warp
-  float steps[kChunkThreads / 32];
-  int unit[2];       // request, unit within it
+  uint64_t q_full;
+  uint64_t q_conv;                 // e4m3: Q converted to fp16 in place (all softmax threads)
+  uint64_t k_full[kFwdStages];     // e4m3: two arrivals, of the widening warps
+  uint64_t v_full[kFwdStages];
+  uint64_t kv_empty[kFwdStages];
+  uint64_t codes_full[kChunkSlots];
+  uint64_t codes_empty[kChunkSlots];
+  uint64_t s_full[kChunkTiles<kF8>];
+  uint64_t p_full[kChunkTiles<kF8>];
+  uint64_t o_full;
+  int units[kChunkThreads<kF8> / 32];  // sums per warp
+  float steps[kChunkThreads<kF8> / 32];
+  int unit[2];                     // request, unit within it
+  uint32_t tmem_base;
+  int abort;
 };
 
 template <bool kF8>
 constexpr size_t chunk_smem_bytes() {
-  return 1024 + kTileBytes * (2 + 2 * kFwdStages) + (kF8 ? kChunkSlots * kChunkSlotBytes : 0) + sizeof(ChunkCtl);
+  return 1024 + kTileBytes * (kChunkTiles<kF8> + 2 * kFwdStages) + (kF8 ? kChunkSlots * kChunkSlotBytes : 0) +
+         sizeof(ChunkCtl<kF8>);
 }
 
-// Tile pairs of a request, and about how many 64-key steps one of its units has.
-__device__ __forceinline__ int chunk_pairs(const ChunkParams& p, const PagedRequest& r) {
-  return r.n > p.a.few ? (r.n + 2 * p.tokens - 1) / (2 * p.tokens) : 0;
+// A request's units of one head, and about how many 64-key steps each has.
+template <bool kF8>
+__device__ __forceinline__ int chunk_units(const ChunkParams& p, const PagedRequest& r) {
+  const int tokens = kChunkTiles<kF8> * p.tokens;
+  return r.n > p.a.few ? (r.n + tokens - 1) / tokens : 0;
 }
+template <bool kF8>
 __device__ __forceinline__ int chunk_steps(const ChunkParams& p, const PagedRequest& r) {
   const int keys = max(r.len - r.n / 2, 1);
-  return (p.a.window > 0 ? min(keys, p.a.window + 2 * p.tokens) : keys) / kHalfN + 1;
+  return (p.a.window > 0 ? min(keys, p.a.window + kChunkTiles<kF8> * p.tokens) : keys) / kHalfN + 1;
 }
 
 // Parts of each of the `rest` units behind the last full wave, of about
 // `steps` steps each: the k of k = floor(w waves / rest) with the least
 // w (steps / k + fixed).
-__host__ __device__ inline int chunk_parts(int rest, int steps) {
+__device__ __forceinline__ int chunk_parts(int rest, int steps, int wave) {
   int best = 1;
   float least = static_cast<float>(steps + kChunkFixed);
-  for (int w = 1; rest > 0 && w <= kChunkMaxParts / kChunkWave; ++w) {
-    int k = w * kChunkWave / rest;
-    if (k > steps / kChunkFixed) k = steps / kChunkFixed;
+  for (int w = 1; w <= kChunkMaxWaves; ++w) {
+    const int k = min(w * wave / rest, steps / kChunkFixed);
     if (k < 2) continue;
     const float cost = w * (static_cast<float>(steps) / k + 2 * kChunkFixed);
     if (cost < least) least = cost, best = k;
@@ -94,8 +115,8 @@ __host__ __device__ inline int chunk_parts(int rest, int steps) {
 
 // Sums over a CTA's threads, in an order that all CTAs share: upto, the units
 // of the threads up to this one, and the totals.
-template <int kWarps>
-__device__ __forceinline__ void chunk_scan(ChunkCtl* cc, int units, float steps, int& upto, int& all_units,
+template <bool kF8>
+__device__ __forceinline__ void chunk_scan(ChunkCtl<kF8>* cc, int units, float steps, int& upto, int& all_units,
                                            float& all_steps) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   upto = units;
@@ -110,7 +131,7 @@ __device__ __forceinline__ void chunk_scan(ChunkCtl* cc, int units, float steps,
   all_units = 0;
   all_steps = 0.f;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
+  for (int w = 0; w < kChunkThreads<kF8> / 32; ++w) {
     if (w < warp) upto += cc->units[w];
     all_units += cc->units[w];
     all_steps += cc->steps[w];
@@ -118,18 +139,20 @@ __device__ __forceinline__ void chunk_scan(ChunkCtl* cc, int units, float steps,
 }
 
 template <bool kF8>
-__global__ void __launch_bounds__(kChunkThreads, 2)
+__global__ void __launch_bounds__(kChunkThreads<kF8>, kChunkPerSm<kF8>)
     sink_attn_paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                                  const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ ChunkParams p) {
-  constexpr int kThreads = kChunkThreads;
+  constexpr int kThreads = kChunkThreads<kF8>;
+  constexpr int kTiles = kChunkTiles<kF8>;
+  constexpr int kMmaWarp = 4 * kTiles, kCopyWarp = kMmaWarp + 1;
+  constexpr uint32_t kTmemO = kTiles * kHalfN;  // columns: S / P of each tile, then O of each
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align1024(smem_raw);
   uint8_t* sQ = smem;
-  uint8_t* sK = smem + 2 * kTileBytes;
+  uint8_t* sK = smem + kTiles * kTileBytes;
   uint8_t* sV = sK + kFwdStages * kTileBytes;
   uint8_t* sB = sV + kFwdStages * kTileBytes;
-  ChunkCtl* cc = reinterpret_cast<ChunkCtl*>(sB + (kF8 ? kChunkSlots * kChunkSlotBytes : 0));
-  FwdCtl* ctl = &cc->f;
+  auto* ctl = reinterpret_cast<ChunkCtl<kF8>*>(sB + (kF8 ? kChunkSlots * kChunkSlotBytes : 0));
   volatile int* abort = &ctl->abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_launch_dependents();
@@ -137,7 +160,7 @@ __global__ void __launch_bounds__(kChunkThreads, 2)
   // ------------------------------------------------------- which unit, which part
   int unit, part, parts, slot;
   PagedRequest rq;
-  int b, pair, g;
+  int b, group, g;
   {
     const int per = (p.a.batch + kThreads - 1) / kThreads;
     const int b0 = threadIdx.x * per;
@@ -146,15 +169,15 @@ __global__ void __launch_bounds__(kChunkThreads, 2)
     for (int i = 0; i < per && b0 + i < p.a.batch; ++i) {
       if (blockIdx.x == 0) paged_check(p.a, b0 + i);
       const PagedRequest r = paged_request(p.a, b0 + i);
-      const int n = chunk_pairs(p, r) * p.a.Hkv;
+      const int n = chunk_units<kF8>(p, r) * p.a.Hkv;
       units += n;
-      steps += static_cast<float>(n) * chunk_steps(p, r);
+      steps += static_cast<float>(n) * chunk_steps<kF8>(p, r);
     }
     int upto, total;
     float all_steps;
-    chunk_scan<kThreads / 32>(cc, units, steps, upto, total, all_steps);
-    const int full = total / kChunkWave * kChunkWave, rest = total - full;
-    parts = p.part_o && rest ? chunk_parts(rest, static_cast<int>(all_steps / total)) : 1;
+    chunk_scan<kF8>(ctl, units, steps, upto, total, all_steps);
+    const int full = total / p.wave * p.wave, rest = total - full;
+    parts = p.part_o && rest ? chunk_parts(rest, static_cast<int>(all_steps / total), p.wave) : 1;
     if (blockIdx.x == 0 && threadIdx.x == 0 && p.part_units) *p.part_units = parts > 1 ? rest : 0;
     unit = blockIdx.x;
     part = 0;
@@ -170,10 +193,10 @@ __global__ void __launch_bounds__(kChunkThreads, 2)
     int at = upto - units;
     if (unit >= at && unit < upto) {
       for (int i = 0;; ++i) {
-        const int n = chunk_pairs(p, paged_request(p.a, b0 + i)) * p.a.Hkv;
+        const int n = chunk_units<kF8>(p, paged_request(p.a, b0 + i)) * p.a.Hkv;
         if (unit < at + n) {
-          cc->unit[0] = b0 + i;
-          cc->unit[1] = unit - at;
+          ctl->unit[0] = b0 + i;
+          ctl->unit[1] = unit - at;
           break;
         }
         at += n;
@@ -181,38 +204,41 @@ __global__ void __launch_bounds__(kChunkThreads, 2)
     }
     if (threadIdx.x == 0) {
       mbar_init(&ctl->q_full, 1);
-      mbar_init(&cc->q_conv, 2 * kBlockM);
+      mbar_init(&ctl->q_conv, kTiles * kBlockM);
       for (int s = 0; s < kFwdStages; ++s) {
-        mbar_init(&ctl->k_full[s], 1);
-        mbar_init(&ctl->v_full[s], 1);
+        mbar_init(&ctl->k_full[s], kF8 ? 2 : 1);
+        mbar_init(&ctl->v_full[s], kF8 ? 2 : 1);
         mbar_init(&ctl->kv_empty[s], 1);
       }
-      for (int w = 0; w < 2; ++w) {
+      for (int w = 0; w < kTiles; ++w) {
         mbar_init(&ctl->s_full[w], 1);
         mbar_init(&ctl->p_full[w], kBlockM);
       }
       mbar_init(&ctl->o_full, 1);
-      for (int s = 0; s < kChunkSlots; ++s) mbar_init(&cc->codes[s], 1);
+      for (int s = 0; s < kChunkSlots; ++s) {
+        mbar_init(&ctl->codes_full[s], 1);
+        mbar_init(&ctl->codes_empty[s], 1);
+      }
       ctl->abort = 0;
       fence_mbar_init();
     }
-    if (warp == kChunkMmaWarp) {
-      tmem_alloc(&ctl->tmem_base, kFwdTmemCols);
+    if (warp == kMmaWarp) {
+      tmem_alloc(&ctl->tmem_base, 2 * kTmemO);
       tmem_relinquish();
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    b = cc->unit[0];
+    b = ctl->unit[0];
     rq = paged_request(p.a, b);
-    const int at_unit = cc->unit[1];
+    const int at_unit = ctl->unit[1];
     g = at_unit % p.a.Hkv;
-    pair = chunk_pairs(p, rq) - 1 - at_unit / p.a.Hkv;
+    group = chunk_units<kF8>(p, rq) - 1 - at_unit / p.a.Hkv;
   }
   const uint32_t tmem = ctl->tmem_base;
   const int G = p.a.G, base = rq.len - rq.n;  // position of the request's first new token
-  const int i0 = pair * 2 * p.tokens;         // the pair's first token within the request
-  const int key_hi = base + min(i0 + 2 * p.tokens, rq.n) - 1;  // the last key any row sees
+  const int i0 = group * kTiles * p.tokens;   // the unit's first token within the request
+  const int key_hi = base + min(i0 + kTiles * p.tokens, rq.n) - 1;  // the last key any row sees
   const int box_log2 = p.a.box_log2;
   const int key_lo = p.a.window > 0 ? max(0, base + i0 - p.a.window + 1) >> box_log2 << box_log2 : 0;
   // This part's 128-key tiles and 64-key steps.
@@ -223,23 +249,23 @@ __global__ void __launch_bounds__(kChunkThreads, 2)
   const int n_half = min(halves - 2 * tile0, 2 * n_tiles);
   const int key0 = key_lo + tile0 * kBlockN;
 
-  if (warp >= kChunkMmaWarp) {
-    if (warp == kChunkMmaWarp) {
+  if (warp >= kMmaWarp) {
+    if (warp == kMmaWarp) {
       // ---------------------------------------------------------- MMA issuer
-      // As in the two-tile forward: S_b(h) -> P_b(h) -> O_b += P_b V(h) ->
+      // As in the two-tile forward, the tiles in turn: S_b(h) -> P_b(h) -> O_b += P_b V(h) ->
       // S_b(h+1) into the buffer that P_b(h) just left.
       if (n_half > 0 && elect_one()) {
-        mbar_arrive_expect_tx(&ctl->q_full, 2 * p.tokens * G * kHeadDim * 2);
-        for (int u = 0; u < 2; ++u)
+        mbar_arrive_expect_tx(&ctl->q_full, kTiles * p.tokens * G * kHeadDim * 2);
+        for (int u = 0; u < kTiles; ++u)
           tma_load_3d(sQ + u * kTileBytes, &tm_q, &ctl->q_full, 0, g * G, rq.t0 + i0 + u * p.tokens);
-        const uint32_t tS = tmem + kFwdTmemS;
-        const uint32_t tO = tmem + kFwdTmemO;
-        bool ok = mbar_wait(kF8 ? &cc->q_conv : &ctl->q_full, 0, abort, &g_device_error, kDevErrTimeoutMma) &&
+        const uint32_t tS = tmem;
+        const uint32_t tO = tmem + kTmemO;
+        bool ok = mbar_wait(kF8 ? &ctl->q_conv : &ctl->q_full, 0, abort, &g_device_error, kDevErrTimeoutMma) &&
                   mbar_wait(&ctl->k_full[0], 0, abort, &g_device_error, kDevErrTimeoutMma);
         if (ok) {
           tc_fence_after();
 #pragma unroll
-          for (int w = 0; w < 2; ++w) {
+          for (int w = 0; w < kTiles; ++w) {
             fwd_issue_qk<kF8>(tS + w * kHalfN, smem_u32(sQ + w * kTileBytes), smem_u32(sK));
             tc_commit(&ctl->s_full[w]);
           }
@@ -250,7 +276,7 @@ __global__ void __launch_bounds__(kChunkThreads, 2)
           ok = mbar_wait(&ctl->v_full[s], (j / kFwdStages) & 1, abort, &g_device_error, kDevErrTimeoutMma) &&
                (hn >= n_half ||
                 mbar_wait(&ctl->k_full[sn], (jn / kFwdStages) & 1, abort, &g_device_error, kDevErrTimeoutMma));
-          for (int w = 0; ok && w < 2; ++w) {
+          for (int w = 0; ok && w < kTiles; ++w) {
             ok = mbar_wait(&ctl->p_full[w], h & 1, abort, &g_device_error, kDevErrTimeoutMma);
             if (!ok) break;
             tc_fence_after();
@@ -266,7 +292,7 @@ __global__ void __launch_bounds__(kChunkThreads, 2)
         }
         if (ok) tc_commit(&ctl->o_full);
       }
-    } else if constexpr (!kF8) {
+    } else if (!kF8 && warp == kCopyWarp) {
       // ---------------------------------------------------------- TMA producer
       // Lane x looks up the page of box x, a tile ahead of the copies.
       const int nbox = kBlockN >> box_log2, page_mask = (1 << p.a.page_log2) - 1;
@@ -298,25 +324,28 @@ __global__ void __launch_bounds__(kChunkThreads, 2)
           __syncwarp();
         }
       }
-    } else {
-      // -------------------------------------------------- e4m3: copy and widen
+    } else if (kF8 && warp == kCopyWarp) {
+      // ------------------------------------------------------ e4m3: TMA producer
       // Slot q holds 32 keys: of tile q / 8 those of K, four slots, then those
-      // of V.  Rows that no row of the request sees become zeros.
+      // of V.
       const int nbox = kBlockN >> box_log2, page_mask = (1 << p.a.page_log2) - 1;
       const int per_slot = kChunkSlotKeys >> box_log2;
       auto wanted = [&](int j) { return lane < nbox && key0 + j * kBlockN + (lane << box_log2) <= key_hi; };
       auto entry = [&](int j) { return paged_entry(p.a, b, key0 + j * kBlockN + (lane << box_log2)); };
       int next = wanted(0) ? entry(0) : 0, mine = 0;
-      const int slots = 8 * n_tiles;
-      int issued = 0;
-      auto fetch = [&]() {  // by the whole warp
-        const int j = issued >> 3, e = issued & 7;
+      bool ok = true;
+      for (int q = 0; ok && q < 8 * n_tiles; ++q) {
+        const int j = q >> 3, e = q & 7, at_slot = q % kChunkSlots;
         if (e == 0) {
           mine = wanted(j) ? paged_page(p.a, next) : p.a.num_pages;
           if (j + 1 < n_tiles && wanted(j + 1)) next = entry(j + 1);
         }
-        uint64_t* full = &cc->codes[issued % kChunkSlots];
-        uint8_t* to = sB + issued % kChunkSlots * kChunkSlotBytes;
+        if (q >= kChunkSlots)
+          ok = warp_all(mbar_wait(&ctl->codes_empty[at_slot], ((q / kChunkSlots) - 1) & 1, abort, &g_device_error,
+                                  kDevErrTimeoutProducer));
+        if (!ok) break;
+        uint64_t* full = &ctl->codes_full[at_slot];
+        uint8_t* to = sB + at_slot * kChunkSlotBytes;
         if (elect_one()) mbar_arrive_expect_tx(full, kChunkSlotBytes);
         __syncwarp();
         for (int x = 0; x < per_slot; ++x) {
@@ -327,24 +356,25 @@ __global__ void __launch_bounds__(kChunkThreads, 2)
             tma_load_4d(to + (x << box_log2) * kHeadDim, e < 4 ? &tm_k : &tm_v, full, 0, at, g, page);
           __syncwarp();
         }
-        ++issued;
-      };
-      while (issued < min(kChunkSlots, slots)) fetch();
+      }
+    } else if (kF8) {
+      // ------------------------------------------------------------ e4m3: widen
+      // This warp takes every other slot.  Rows that no row of the request sees
+      // become zeros.
       bool ok = true;
-      int q = 0;
-      for (; q < slots; ++q) {
-        const int j = q >> 3, e = q & 7, s = j % kFwdStages, slot_q = q % kChunkSlots;
-        if (e == 0 && j >= kFwdStages)
+      for (int q = warp - kCopyWarp - 1; q < 8 * n_tiles; q += 2) {
+        const int j = q >> 3, e = q & 7, s = j % kFwdStages, at_slot = q % kChunkSlots;
+        if (e < 2 && j >= kFwdStages)
           ok = warp_all(mbar_wait(&ctl->kv_empty[s], ((j / kFwdStages) - 1) & 1, abort, &g_device_error,
                                   kDevErrTimeoutProducer));
-        ok = ok && warp_all(mbar_wait(&cc->codes[slot_q], (q / kChunkSlots) & 1, abort, &g_device_error,
+        ok = ok && warp_all(mbar_wait(&ctl->codes_full[at_slot], (q / kChunkSlots) & 1, abort, &g_device_error,
                                       kDevErrTimeoutProducer));
         if (!ok) break;
         uint4 v[4];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {  // 16 codes: row lane / 4 + 8 u, 16-byte piece lane % 4
           const int row = (lane >> 2) + 8 * u;
-          v[u] = *reinterpret_cast<const uint4*>(sB + slot_q * kChunkSlotBytes + row * kHeadDim +
+          v[u] = *reinterpret_cast<const uint4*>(sB + at_slot * kChunkSlotBytes + row * kHeadDim +
                                                  (((lane & 3) ^ ((row >> 1) & 3)) << 4));
         }
         uint8_t* tile = (e < 4 ? sK : sV) + s * kTileBytes + (e & 3) * kChunkSlotKeys * 128;
@@ -362,16 +392,9 @@ __global__ void __launch_bounds__(kChunkThreads, 2)
         }
         fence_proxy_async_smem();  // the tile for the MMA; the slot's reads before its next copy
         __syncwarp();
-        if ((e & 3) == 3 && lane == 0) mbar_arrive(e < 4 ? &ctl->k_full[s] : &ctl->v_full[s]);
-        if (issued < slots) fetch();
-      }
-      if (!ok) {
-        // Copies in flight still write to this CTA's shared memory.
-        for (; q < issued; ++q) {
-          const uint64_t t0 = global_timer_ns();
-          while (!mbar_try_wait(&cc->codes[q % kChunkSlots], (q / kChunkSlots) & 1) &&
-                 global_timer_ns() - t0 < kWaitLimitNs / 4) {
-          }
+        if (lane == 0) {
+          mbar_arrive(&ctl->codes_empty[at_slot]);
+          if ((e & 3) >= 2) mbar_arrive(e < 4 ? &ctl->k_full[s] : &ctl->v_full[s]);
         }
       }
     }
@@ -392,8 +415,8 @@ __global__ void __launch_bounds__(kChunkThreads, 2)
     const int all_lo = p.a.window > 0 ? max(0, base + w1 - p.a.window + 1) : 0;
     float m_ref = -INFINITY, l = 0.f;
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t tS = tmem + lane_base + kFwdTmemS + wg * kHalfN;
-    const uint32_t tO = tmem + lane_base + kFwdTmemO + wg * kHeadDim;
+    const uint32_t tS = tmem + lane_base + wg * kHalfN;
+    const uint32_t tO = tmem + lane_base + kTmemO + wg * kHeadDim;
     const float sl2 = kF8 ? p.a.scale_log2 * __ldg(p.a.k_scale + g) : p.a.scale_log2;
     bool ok = n_half > 0;  // a part of a unit with fewer tiles than parts may have none
     if constexpr (kF8) {
@@ -407,7 +430,7 @@ __global__ void __launch_bounds__(kChunkThreads, 2)
           row[at] = bf16x2_to_f16x2_sat(row[at]);
         }
         fence_proxy_async_smem();
-        mbar_arrive(&cc->q_conv);
+        mbar_arrive(&ctl->q_conv);
       }
     }
 
@@ -457,8 +480,8 @@ __global__ void __launch_bounds__(kChunkThreads, 2)
 
     // ---------------------------------------------------------------- epilogue
     if (n_half == 0) {
-      p.part_ml[static_cast<long long>(slot) * 2 * kBlockM + wg * kBlockM + r] = make_float2(-INFINITY, 0.f);
-      if (part == 0 && threadIdx.x == 0) p.part_unit[slot / parts] = make_int4(b, pair, g, parts);
+      p.part_ml[static_cast<long long>(slot) * kTiles * kBlockM + wg * kBlockM + r] = make_float2(-INFINITY, 0.f);
+      if (part == 0 && threadIdx.x == 0) p.part_unit[slot / parts] = make_int4(b, group, g, parts);
     }
     if (ok) ok = mbar_wait(&ctl->o_full, 0, abort, &g_device_error, kDevErrTimeoutEpilogue);
     ok = warp_all(ok);
@@ -469,9 +492,9 @@ __global__ void __launch_bounds__(kChunkThreads, 2)
       tmem_ld64(tO, o);
       const float vs = kF8 ? __ldg(p.a.v_scale + g) : 1.f;
       if (parts > 1) {
-        const long long at = static_cast<long long>(slot) * 2 * kBlockM + wg * kBlockM + r;
+        const long long at = static_cast<long long>(slot) * kTiles * kBlockM + wg * kBlockM + r;
         p.part_ml[at] = make_float2(m_ref, l);
-        if (part == 0 && threadIdx.x == 0) p.part_unit[slot / parts] = make_int4(b, pair, g, parts);
+        if (part == 0 && threadIdx.x == 0) p.part_unit[slot / parts] = make_int4(b, group, g, parts);
         float4* dst = reinterpret_cast<float4*>(p.part_o + at * kHeadDim);
         if (valid) {
 #pragma unroll
@@ -506,26 +529,28 @@ __global__ void __launch_bounds__(kChunkThreads, 2)
 
   tc_fence_before();
   __syncthreads();
-  if (warp == kChunkMmaWarp) {
+  if (warp == kMmaWarp) {
     tc_fence_after();
-    tmem_dealloc(tmem, kFwdTmemCols);
+    tmem_dealloc(tmem, 2 * kTmemO);
   }
 }
 
 // Joins the parts of the cut units and adds the sink.  One CTA per cut unit
-// and 32 of its 256 rows; half a warp per row, four dims per lane.
+// and 32 of its rows; half a warp per row, four dims per lane.
+template <bool kF8>
 __global__ void __launch_bounds__(256) sink_attn_paged_chunk_join_kernel(const __grid_constant__ ChunkParams p) {
   pdl_wait();
   const int i = blockIdx.x;
   if (i >= __ldcg(p.part_units)) return;
   const int4 u = __ldcg(p.part_unit + i);
   const PagedRequest rq = paged_request(p.a, u.x);
+  constexpr int kTiles = kChunkTiles<kF8>;
   const int d = threadIdx.x & 15;
 #pragma unroll
   for (int x = 0; x < 2; ++x) {
     const int row = blockIdx.y * 32 + x * 16 + (threadIdx.x >> 4);
     const int r = row & (kBlockM - 1), row_t = r / p.a.G;
-    const int it = (2 * u.y + (row >> 7)) * p.tokens + row_t;
+    const int it = (kTiles * u.y + (row >> 7)) * p.tokens + row_t;
     if (row_t >= p.tokens || it >= rq.n) continue;
     const int h = u.z * p.a.G + r - row_t * p.a.G;
     const float s2 = __ldg(p.a.sinks + h) * kLog2e;
@@ -533,7 +558,7 @@ __global__ void __launch_bounds__(256) sink_attn_paged_chunk_join_kernel(const _
     float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
     for (int k = 0; k < u.w; ++k) {
-      const long long at = (static_cast<long long>(i) * u.w + k) * 2 * kBlockM + row;
+      const long long at = (static_cast<long long>(i) * u.w + k) * kTiles * kBlockM + row;
       const float2 ml = __ldcg(p.part_ml + at);
       const float4 v = __ldcg(reinterpret_cast<const float4*>(p.part_o + at * kHeadDim) + d);
       const float now = fmaxf(m, ml.x);

@@ -688,15 +688,17 @@ struct ChunkBound {
   int64_t units, parts;
 };
 
+template <bool kF8>
 ChunkBound chunk_bound(const sink_attn_paged_dims* d, const PagedSplit& s, int window) {
   ChunkBound c;
-  const int tokens = kBlockM / (d->num_q_heads / d->num_kv_heads);
+  const int tokens = kChunkTiles<kF8> * (kBlockM / (d->num_q_heads / d->num_kv_heads));  // of a unit
   const int64_t requests = std::min<int64_t>(d->batch, d->total_tokens / (s.few + 1));
-  c.units = d->num_kv_heads * (d->total_tokens / (2 * tokens) + requests);
+  c.units = d->num_kv_heads * (d->total_tokens / tokens + requests);
   const int64_t keys = std::min<int64_t>(int64_t(d->max_pages) * d->page_size,
-                                         window > 0 ? int64_t(window) + 2 * tokens : INT64_MAX);
+                                         window > 0 ? int64_t(window) + tokens : INT64_MAX);
   const int64_t most = (keys / kHalfN + 1) / kChunkFixed;  // parts of a unit
-  c.parts = most < 2 ? 0 : std::min<int64_t>(kChunkMaxParts, std::min<int64_t>(c.units, kChunkWave) * most);
+  const int64_t wave = kChunkPerSm<kF8> * kChunkSms;
+  c.parts = most < 2 ? 0 : std::min(kChunkMaxWaves * wave, std::min(c.units, wave) * most);
   return c;
 }
 
@@ -722,9 +724,11 @@ PagedWorkspace paged_workspace(const sink_attn_paged_dims* d, const PagedSplit& 
     w.o = take(rows * kHeadDim * sizeof(float));
   }
   if (s.chunks) {
-    const size_t rows = static_cast<size_t>(chunk_bound(d, s, 0).parts) * 2 * kBlockM;
+    // (Rows of parts: for either type of cache.)
+    const size_t rows = static_cast<size_t>(std::max(chunk_bound<false>(d, s, 0).parts * kChunkTiles<false>,
+                                                     chunk_bound<true>(d, s, 0).parts * kChunkTiles<true>)) * kBlockM;
     w.chunk_units = take(sizeof(int));
-    w.chunk_unit = take(kChunkWave * sizeof(int4));
+    w.chunk_unit = take(kChunkPerSm<false> * kChunkSms * sizeof(int4));
     w.chunk_ml = take(rows * sizeof(float2));
     w.chunk_o = take(rows * kHeadDim * sizeof(float));
   }
@@ -822,7 +826,10 @@ bool make_map_paged_q(CUtensorMap* map, const sink_attn_paged_dims* d, const voi
 
 template <bool kF8>
 bool launch_chunks(ChunkParams& p, const sink_attn_paged_dims* d, const void* k_cache, const void* v_cache,
-                   const ChunkBound& bound, cudaStream_t st) {
+                   const PagedSplit& split, cudaStream_t st) {
+  const ChunkBound bound = chunk_bound<kF8>(d, split, p.a.window);
+  if (bound.units + bound.parts > 0x7fffffff) return false;
+  p.wave = kChunkPerSm<kF8> * kChunkSms;
   CUtensorMap tm_q, tm_k, tm_v;
   const int box = std::min(d->page_size, kF8 ? kChunkSlotKeys : kHalfN);
   p.a.box_log2 = ilog2_exact(box);
@@ -832,12 +839,12 @@ bool launch_chunks(ChunkParams& p, const sink_attn_paged_dims* d, const void* k_
   static SmemAttrOnce smem_set;
   if (!smem_set.ensure(sink_attn_paged_chunk_kernel<kF8>, chunk_smem_bytes<kF8>())) return false;
   if (bound.parts == 0) p.part_o = nullptr;
-  sink_attn_paged_chunk_kernel<kF8><<<static_cast<unsigned>(bound.units + bound.parts), kChunkThreads,
+  sink_attn_paged_chunk_kernel<kF8><<<static_cast<unsigned>(bound.units + bound.parts), kChunkThreads<kF8>,
                                       chunk_smem_bytes<kF8>(), st>>>(tm_q, tm_k, tm_v, p);
   if (cudaPeekAtLastError() != cudaSuccess) return false;
   if (bound.parts == 0) return true;
-  const unsigned cut = static_cast<unsigned>(std::min<int64_t>(bound.units, kChunkWave - 1));
-  return launch_join(sink_attn_paged_chunk_join_kernel, dim3(cut, 2 * kBlockM / 32), p, st);
+  const unsigned cut = static_cast<unsigned>(std::min<int64_t>(bound.units, p.wave - 1));
+  return launch_join(sink_attn_paged_chunk_join_kernel<kF8>, dim3(cut, kChunkTiles<kF8> * kBlockM / 32), p, st);
 }
 
 sink_attn_status paged_attn_impl(const sink_attn_paged_dims* d, const void* q, const void* k_cache,
@@ -899,10 +906,8 @@ sink_attn_status paged_attn_impl(const sink_attn_paged_dims* d, const void* q, c
     c.part_unit = reinterpret_cast<int4*>(base + ws.chunk_unit);
     c.part_ml = reinterpret_cast<float2*>(base + ws.chunk_ml);
     c.part_o = reinterpret_cast<float*>(base + ws.chunk_o);
-    const ChunkBound bound = chunk_bound(d, split, p.window);
-    if (bound.units + bound.parts > 0x7fffffff) return SINK_ATTN_ERR_UNSUPPORTED;
-    if (!(codes ? launch_chunks<true>(c, d, k_cache, v_cache, bound, st_)
-                : launch_chunks<false>(c, d, k_cache, v_cache, bound, st_)))
+    if (!(codes ? launch_chunks<true>(c, d, k_cache, v_cache, split, st_)
+                : launch_chunks<false>(c, d, k_cache, v_cache, split, st_)))
       return SINK_ATTN_ERR_CUDA;
   }
   if (split.rows && !(codes ? launch_rows<true>(split.kR, p, d, k_cache, v_cache, st_)
