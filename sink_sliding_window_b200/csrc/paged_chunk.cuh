@@ -21,7 +21,7 @@
 // of V are zeroed in shared memory by the softmax threads of the steps that
 // hold such keys, since 0 * NaN is not 0.
 //
-// e4m3: the codes come by TMA into a ring of 2 KB slots, and two warps write
+// e4m3: the codes come by TMA into a ring of 4 KB slots, and two warps write
 // them widened to fp16 (exactly) into the same tiles that TMA fills for bf16.
 // Widening costs as much for two query tiles as for four, so one CTA of four
 // tiles and twenty warps takes the place of two CTAs of two tiles and ten
@@ -47,8 +47,8 @@ constexpr int kChunkPerSm = kF8 ? 1 : 2;
 constexpr int kChunkSms = 148;
 constexpr int kChunkMaxWaves = 3;  // of parts
 constexpr int kChunkFixed = 8;     // a part's set-up, ends and join, in 64-key steps
-constexpr int kChunkSlots = 8;
-constexpr int kChunkSlotKeys = 32;
+constexpr int kChunkSlots = 4;
+constexpr int kChunkSlotKeys = 64;
 constexpr int kChunkSlotBytes = kChunkSlotKeys * kHeadDim;  // e4m3 codes of K or V
 
 struct ChunkParams {
@@ -104,11 +104,13 @@ __device__ __forceinline__ int chunk_steps(const ChunkParams& p, const PagedRequ
 __device__ __forceinline__ int chunk_parts(int rest, int steps, int wave) {
   int best = 1;
   float least = static_cast<float>(steps + kChunkFixed);
+#pragma unroll
   for (int w = 1; w <= kChunkMaxWaves; ++w) {
-    const int k = min(w * wave / rest, steps / kChunkFixed);
-    if (k < 2) continue;
-    const float cost = w * (static_cast<float>(steps) / k + 2 * kChunkFixed);
-    if (cost < least) least = cost, best = k;
+    int k = static_cast<int>(__fdividef(static_cast<float>(w * wave), static_cast<float>(rest)) + 0.01f);
+    if (k * rest > w * wave) --k;
+    k = min(k, steps / kChunkFixed);
+    const float cost = w * (__fdividef(static_cast<float>(steps), static_cast<float>(k)) + 2 * kChunkFixed);
+    if (k >= 2 && cost < least) least = cost, best = k;
   }
   return best;
 }
@@ -136,6 +138,12 @@ __device__ __forceinline__ void chunk_scan(ChunkCtl<kF8>* cc, int units, float s
     all_units += cc->units[w];
     all_steps += cc->steps[w];
   }
+}
+
+// Bits lo .. hi of a word (both inclusive and possibly outside of it).
+__device__ __forceinline__ uint32_t chunk_bits(int lo, int hi) {
+  const uint32_t from = lo <= 0 ? 0xFFFFFFFFu : lo > 31 ? 0u : 0xFFFFFFFFu << lo;
+  return hi < 0 ? 0u : hi >= 31 ? from : from & (0xFFFFFFFFu >> (31 - hi));
 }
 
 template <bool kF8>
@@ -204,7 +212,7 @@ __global__ void __launch_bounds__(kChunkThreads<kF8>, kChunkPerSm<kF8>)
     }
     if (threadIdx.x == 0) {
       mbar_init(&ctl->q_full, 1);
-      mbar_init(&ctl->q_conv, kTiles * kBlockM);
+      mbar_init(&ctl->q_conv, kTiles * kBlockM);  // every softmax thread, with or without rows
       for (int s = 0; s < kFwdStages; ++s) {
         mbar_init(&ctl->k_full[s], kF8 ? 2 : 1);
         mbar_init(&ctl->v_full[s], kF8 ? 2 : 1);
@@ -248,6 +256,8 @@ __global__ void __launch_bounds__(kChunkThreads<kF8>, kChunkPerSm<kF8>)
   const int n_tiles = static_cast<int>(static_cast<int64_t>(tiles) * (part + 1) / parts) - tile0;
   const int n_half = min(halves - 2 * tile0, 2 * n_tiles);
   const int key0 = key_lo + tile0 * kBlockN;
+  // Tiles that hold tokens: the last unit of a request may have fewer than kTiles.
+  const int live = min(kTiles, (rq.n - i0 + p.tokens - 1) / p.tokens);
 
   if (warp >= kMmaWarp) {
     if (warp == kMmaWarp) {
@@ -266,6 +276,7 @@ __global__ void __launch_bounds__(kChunkThreads<kF8>, kChunkPerSm<kF8>)
           tc_fence_after();
 #pragma unroll
           for (int w = 0; w < kTiles; ++w) {
+            if (w >= live) break;
             fwd_issue_qk<kF8>(tS + w * kHalfN, smem_u32(sQ + w * kTileBytes), smem_u32(sK));
             tc_commit(&ctl->s_full[w]);
           }
@@ -276,7 +287,7 @@ __global__ void __launch_bounds__(kChunkThreads<kF8>, kChunkPerSm<kF8>)
           ok = mbar_wait(&ctl->v_full[s], (j / kFwdStages) & 1, abort, &g_device_error, kDevErrTimeoutMma) &&
                (hn >= n_half ||
                 mbar_wait(&ctl->k_full[sn], (jn / kFwdStages) & 1, abort, &g_device_error, kDevErrTimeoutMma));
-          for (int w = 0; ok && w < kTiles; ++w) {
+          for (int w = 0; ok && w < live; ++w) {
             ok = mbar_wait(&ctl->p_full[w], h & 1, abort, &g_device_error, kDevErrTimeoutMma);
             if (!ok) break;
             tc_fence_after();
@@ -313,29 +324,28 @@ __global__ void __launch_bounds__(kChunkThreads<kF8>, kChunkPerSm<kF8>)
           mbar_arrive_expect_tx(&ctl->v_full[s], kTileBytes);
         }
         __syncwarp();
-        for (int x = 0; x < nbox; ++x) {
+        for (int y = 0; y < 2 * nbox; ++y) {  // K first: S waits for it
+          const bool is_v = y >= nbox;
+          const int x = is_v ? y - nbox : y;
           const int page = __shfl_sync(0xffffffffu, mine, x);
           const int at = (key0 + j * kBlockN + (x << box_log2)) & page_mask;
-          if (elect_one()) {
-            const int to = s * kTileBytes + (x << box_log2) * kHeadDim * 2;
-            tma_load_4d(sK + to, &tm_k, &ctl->k_full[s], 0, at, g, page);
-            tma_load_4d(sV + to, &tm_v, &ctl->v_full[s], 0, at, g, page);
-          }
+          if (elect_one())
+            tma_load_4d((is_v ? sV : sK) + s * kTileBytes + (x << box_log2) * kHeadDim * 2, is_v ? &tm_v : &tm_k,
+                        is_v ? &ctl->v_full[s] : &ctl->k_full[s], 0, at, g, page);
           __syncwarp();
         }
       }
     } else if (kF8 && warp == kCopyWarp) {
       // ------------------------------------------------------ e4m3: TMA producer
-      // Slot q holds 32 keys: of tile q / 8 those of K, four slots, then those
-      // of V.
+      // Slot q holds 64 keys: of tile q / 4 those of K, two slots, then those of V.
       const int nbox = kBlockN >> box_log2, page_mask = (1 << p.a.page_log2) - 1;
       const int per_slot = kChunkSlotKeys >> box_log2;
       auto wanted = [&](int j) { return lane < nbox && key0 + j * kBlockN + (lane << box_log2) <= key_hi; };
       auto entry = [&](int j) { return paged_entry(p.a, b, key0 + j * kBlockN + (lane << box_log2)); };
       int next = wanted(0) ? entry(0) : 0, mine = 0;
       bool ok = true;
-      for (int q = 0; ok && q < 8 * n_tiles; ++q) {
-        const int j = q >> 3, e = q & 7, at_slot = q % kChunkSlots;
+      for (int q = 0; ok && q < 4 * n_tiles; ++q) {
+        const int j = q >> 2, e = q & 3, at_slot = q % kChunkSlots;
         if (e == 0) {
           mine = wanted(j) ? paged_page(p.a, next) : p.a.num_pages;
           if (j + 1 < n_tiles && wanted(j + 1)) next = entry(j + 1);
@@ -349,11 +359,11 @@ __global__ void __launch_bounds__(kChunkThreads<kF8>, kChunkPerSm<kF8>)
         if (elect_one()) mbar_arrive_expect_tx(full, kChunkSlotBytes);
         __syncwarp();
         for (int x = 0; x < per_slot; ++x) {
-          const int box = (e & 3) * per_slot + x;
+          const int box = (e & 1) * per_slot + x;
           const int page = __shfl_sync(0xffffffffu, mine, box);
           const int at = (key0 + j * kBlockN + (box << box_log2)) & page_mask;
           if (elect_one())
-            tma_load_4d(to + (x << box_log2) * kHeadDim, e < 4 ? &tm_k : &tm_v, full, 0, at, g, page);
+            tma_load_4d(to + (x << box_log2) * kHeadDim, e < 2 ? &tm_k : &tm_v, full, 0, at, g, page);
           __syncwarp();
         }
       }
@@ -362,25 +372,25 @@ __global__ void __launch_bounds__(kChunkThreads<kF8>, kChunkPerSm<kF8>)
       // This warp takes every other slot.  Rows that no row of the request sees
       // become zeros.
       bool ok = true;
-      for (int q = warp - kCopyWarp - 1; q < 8 * n_tiles; q += 2) {
-        const int j = q >> 3, e = q & 7, s = j % kFwdStages, at_slot = q % kChunkSlots;
+      for (int q = warp - kCopyWarp - 1; q < 4 * n_tiles; q += 2) {
+        const int j = q >> 2, e = q & 3, s = j % kFwdStages, at_slot = q % kChunkSlots;
         if (e < 2 && j >= kFwdStages)
           ok = warp_all(mbar_wait(&ctl->kv_empty[s], ((j / kFwdStages) - 1) & 1, abort, &g_device_error,
                                   kDevErrTimeoutProducer));
         ok = ok && warp_all(mbar_wait(&ctl->codes_full[at_slot], (q / kChunkSlots) & 1, abort, &g_device_error,
                                       kDevErrTimeoutProducer));
         if (!ok) break;
-        uint4 v[4];
+        uint4 v[8];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {  // 16 codes: row lane / 4 + 8 u, 16-byte piece lane % 4
+        for (int u = 0; u < 8; ++u) {  // 16 codes: row lane / 4 + 8 u, 16-byte piece lane % 4
           const int row = (lane >> 2) + 8 * u;
           v[u] = *reinterpret_cast<const uint4*>(sB + at_slot * kChunkSlotBytes + row * kHeadDim +
                                                  (((lane & 3) ^ ((row >> 1) & 3)) << 4));
         }
-        uint8_t* tile = (e < 4 ? sK : sV) + s * kTileBytes + (e & 3) * kChunkSlotKeys * 128;
-        const int key = key0 + j * kBlockN + (e & 3) * kChunkSlotKeys + (lane >> 2);
+        uint8_t* tile = (e < 2 ? sK : sV) + s * kTileBytes + (e & 1) * kChunkSlotKeys * 128;
+        const int key = key0 + j * kBlockN + (e & 1) * kChunkSlotKeys + (lane >> 2);
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
+        for (int u = 0; u < 8; ++u) {
           const int row = (lane >> 2) + 8 * u;
           if (key + 8 * u < rq.lo || key + 8 * u >= rq.len) v[u] = make_uint4(0u, 0u, 0u, 0u);
           const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
@@ -394,7 +404,7 @@ __global__ void __launch_bounds__(kChunkThreads<kF8>, kChunkPerSm<kF8>)
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(&ctl->codes_empty[at_slot]);
-          if ((e & 3) >= 2) mbar_arrive(e < 4 ? &ctl->k_full[s] : &ctl->v_full[s]);
+          mbar_arrive(e < 2 ? &ctl->k_full[s] : &ctl->v_full[s]);
         }
       }
     }
@@ -418,8 +428,11 @@ __global__ void __launch_bounds__(kChunkThreads<kF8>, kChunkPerSm<kF8>)
     const uint32_t tS = tmem + lane_base + wg * kHalfN;
     const uint32_t tO = tmem + lane_base + kTmemO + wg * kHeadDim;
     const float sl2 = kF8 ? p.a.scale_log2 * __ldg(p.a.k_scale + g) : p.a.scale_log2;
-    bool ok = n_half > 0;  // a part of a unit with fewer tiles than parts may have none
+    // A part of a unit with fewer key tiles than parts may have none.
+    bool ok = n_half > 0 && wg < live;
+    const float s2 = valid ? __ldg(p.a.sinks + h) * kLog2e : 0.f;
     if constexpr (kF8) {
+      if (n_half > 0 && wg >= live) mbar_arrive(&ctl->q_conv);
       ok = ok && warp_all(mbar_wait(&ctl->q_full, 0, abort, &g_device_error, kDevErrTimeoutSoftmax));
       if (ok) {
         // Rows of 128 bytes, so elementwise in place whatever the swizzle.
@@ -441,11 +454,14 @@ __global__ void __launch_bounds__(kChunkThreads<kF8>, kChunkPerSm<kF8>)
       uint32_t sr[kHalfN];
       tmem_ld64(tS, sr);
       const int ks = key0 + hs * kHalfN;
-      FwdRowStep st;
-      if (ks + kHalfN - 1 > all_hi || ks < all_lo)
-        st = fwd_row_step<true, kF8>(sr, lo_r - ks, hi_r - ks, sl2, m_ref);
-      else
-        st = fwd_row_step<false, kF8>(sr, 0, 0, sl2, m_ref);
+      if (ks + kHalfN - 1 > all_hi || ks < all_lo) {
+        // One bit per key: a test and a selection each, where two compares of
+        // the key's place made a window layer's steps half as long again.
+        const uint32_t seen[2] = {chunk_bits(lo_r - ks, hi_r - ks), chunk_bits(lo_r - ks - 32, hi_r - ks - 32)};
+#pragma unroll
+        for (int c = 0; c < kHalfN; ++c) sr[c] = seen[c >> 5] >> (c & 31) & 1u ? sr[c] : 0xFF800000u;
+      }
+      const FwdRowStep st = fwd_row_step<false, kF8>(sr, 0, 0, sl2, m_ref);
       l = l * st.alpha + st.sum;
       __syncwarp();
       tmem_st32(tS, sr);
@@ -503,7 +519,6 @@ __global__ void __launch_bounds__(kChunkThreads<kF8>, kChunkPerSm<kF8>)
                                  __uint_as_float(o[4 * c + 2]) * vs, __uint_as_float(o[4 * c + 3]) * vs);
         }
       } else if (valid) {
-        const float s2 = __ldg(p.a.sinks + h) * kLog2e;
         const float top = fmaxf(s2, m_ref);
         float f = 0.f, all = 0.f;
         if (top != -INFINITY) {

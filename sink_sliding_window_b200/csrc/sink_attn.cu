@@ -831,7 +831,7 @@ bool launch_chunks(ChunkParams& p, const sink_attn_paged_dims* d, const void* k_
   if (bound.units + bound.parts > 0x7fffffff) return false;
   p.wave = kChunkPerSm<kF8> * kChunkSms;
   CUtensorMap tm_q, tm_k, tm_v;
-  const int box = std::min(d->page_size, kF8 ? kChunkSlotKeys : kHalfN);
+  const int box = std::min(d->page_size, kHalfN);
   p.a.box_log2 = ilog2_exact(box);
   if (!make_map_paged_q(&tm_q, d, p.a.q, p.a.G, p.tokens) || !make_map_paged(&tm_k, k_cache, d, kF8, box, 1) ||
       !make_map_paged(&tm_v, v_cache, d, kF8, box, 1))
