@@ -1,4 +1,5 @@
-"""Builds libsinkattn.so (the C-ABI library) in-tree with nvcc for sm_100a.
+"""Builds libsinkattn.so (the C-ABI library) in-tree with nvcc for sm_100a, and
+_paged.so, the native binding of its paged-cache calls.
 
     python -m sink_sliding_window_b200.build [--force] [--verbose-ptxas]
 """
@@ -9,12 +10,15 @@ import glob
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libsinkattn.so")
+BINDING = os.path.join(PKG, "_paged.so")
+BINDING_SRC = os.path.join(CSRC, "paged_binding.cpp")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
 
@@ -23,24 +27,48 @@ def _sources():
                   glob.glob(os.path.join(INCLUDE, "*.h")))
 
 
-def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+def _newer(target, sources) -> bool:
+    if not os.path.exists(target):
         return False
-    t = os.path.getmtime(LIB)
-    return all(os.path.getmtime(s) <= t for s in _sources())
+    t = os.path.getmtime(target)
+    return all(os.path.getmtime(s) <= t for s in sources)
+
+
+def up_to_date() -> bool:
+    return _newer(LIB, _sources())
+
+
+def build_binding(force: bool = False) -> str:
+    """_paged.so: compiled by the host compiler against torch's headers, it
+    finds libsinkattn.so beside it."""
+    header = os.path.join(INCLUDE, "sink_attn.h")
+    if not force and _newer(BINDING, [BINDING_SRC, header]):
+        return BINDING
+    import torch
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(NVCC))
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE,
+           "-isystem", os.path.join(root, "include"), "-isystem", os.path.join(cuda, "include"),
+           "-isystem", sysconfig.get_paths()["include"], BINDING_SRC, "-o", tmp, "-L", PKG, "-l:" + os.path.basename(LIB),
+           "-L", os.path.join(root, "lib"), "-lc10", "-ltorch_cpu", "-ltorch_python", "-lc10_cuda", "-Wl,-rpath,$ORIGIN"]
+    subprocess.run(cmd, check=True)
+    os.replace(tmp, BINDING)
+    return BINDING
 
 
 def build(force: bool = False, ptxas_verbose: bool = False) -> str:
-    if not force and up_to_date():
-        return LIB
-    tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [NVCC, "-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", "-std=c++17",
-           "-Xcompiler", "-fPIC", "-shared", "-I", INCLUDE, "-I", CSRC,
-           os.path.join(CSRC, "sink_attn.cu"), "-o", tmp]
-    if ptxas_verbose:
-        cmd.insert(1, "-Xptxas=-v")
-    subprocess.run(cmd, check=True)
-    os.replace(tmp, LIB)
+    if force or not up_to_date():
+        tmp = LIB + f".tmp{os.getpid()}"
+        cmd = [NVCC, "-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", "-std=c++17",
+               "-Xcompiler", "-fPIC", "-shared", "-I", INCLUDE, "-I", CSRC,
+               os.path.join(CSRC, "sink_attn.cu"), "-o", tmp]
+        if ptxas_verbose:
+            cmd.insert(1, "-Xptxas=-v")
+        subprocess.run(cmd, check=True)
+        os.replace(tmp, LIB)
+    build_binding(force)
     return LIB
 
 

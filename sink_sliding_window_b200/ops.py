@@ -2,12 +2,14 @@
 
 Argument marshalling only: shapes and pointers of torch CUDA tensors go in,
 the C-ABI entry points do all the work on the current (or given) stream.
+The paged-cache calls go through a native binding (csrc/paged_binding.cpp)
+of the same kind, since ctypes takes longer than their smaller kernels.
 There is no CPU fallback: if the library is missing, loading raises.
 """
 from __future__ import annotations
 
 import ctypes
-import functools
+import importlib.util
 import os
 
 import torch
@@ -341,82 +343,29 @@ def decode_e4m3_f8pv(*args, **kw):
     return decode_e4m3(*args, f8pv=True, **kw)
 
 
-# The paged calls run many times a step beside kernels of a few microseconds,
-# so their checks are one expression per tensor; _refuse finds the words when
-# one fails.
-_I32 = torch.int32
-_BF16 = torch.bfloat16
-_F32 = torch.float32
-_CODES = (torch.uint8, torch.float8_e4m3fn)
+_paged = None
 
 
-def _refuse(t, name, dtype, shape, device, strides=False):
-    """Raises for a tensor of another type, shape (None: any length) or device
-    than a paged call takes, or, unless strides are the call's to give, one
-    that is not contiguous."""
-    if not t.is_cuda:
-        raise ValueError(f"{name}: expected a CUDA tensor, got one on {t.device}")
-    if t.get_device() != device:
-        raise ValueError(f"{name} is on {t.device}, the call's other tensors are on cuda:{device}")
-    if t.dtype != dtype:
-        raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
-    if t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
-        raise ValueError(f"{name}: expected shape {shape}, got {tuple(t.shape)}")
-    if not strides and not t.is_contiguous():
-        raise ValueError(f"{name} is not contiguous")
-    raise ValueError(f"{name}: not a tensor of this call")
+def _paged_calls():
+    """The native binding of the paged calls (raises if it has not been built)."""
+    global _paged
+    if _paged is None:
+        load()
+        path = os.path.join(os.path.dirname(_LIB_PATH), "_paged.so")
+        if not os.path.exists(path):
+            raise RuntimeError(f"_paged.so not found at {path}; build it with `python -m sink_sliding_window_b200.build`")
+        spec = importlib.util.spec_from_file_location("_paged", path)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        _paged = module
+    return _paged
 
 
-def _check(t, name, dtype, shape, device):
-    """A dense tensor of one type, shape and device."""
-    if t.dtype is not dtype or t.get_device() != device or t.shape != shape or not t.is_contiguous():
-        _refuse(t, name, dtype, shape, device)
-
-
-def _check_heads(t, name, heads, device):
-    """bf16 [T, heads, 64] with contiguous tokens, at any token stride."""
-    if t.dtype is not _BF16 or t.get_device() != device or t.dim() != 3 or t.shape[1] != heads or t.shape[2] != 64:
-        _refuse(t, name, _BF16, (None, heads, 64), device, strides=True)
-    st = t.stride()
-    if st[2] != 1 or (heads > 1 and st[1] != 64):
-        raise ValueError(f"{name}: the heads of a token are not contiguous")
-    return st[0]
-
-
-def _on_stream(call, device, stream):
-    """Runs a paged call with its device current, on the given stream or on
-    that device's current one; what it allocates belongs to that stream."""
-    if stream is None:
-        if device == torch.cuda.current_device():
-            return call(torch._C._cuda_getCurrentRawStream(device))
-        with torch.cuda.device(device):
-            return call(torch._C._cuda_getCurrentRawStream(device))
-    if stream.device.index != device:
-        raise ValueError(f"the stream is on {stream.device}, the tensors are on cuda:{device}")
-    with torch.cuda.stream(stream):
-        return call(stream.cuda_stream)
-
-
-def _paged_cache(k_cache, v_cache, k_scale, v_scale):
-    """Checks a paged cache; returns (codes, device, shape, strides)."""
-    dtype, dev, shape, st = k_cache.dtype, k_cache.get_device(), k_cache.shape, k_cache.stride()
-    codes = dtype in _CODES
-    if not codes and dtype is not _BF16:
-        raise ValueError(f"k_cache: expected bfloat16, float8_e4m3fn or uint8 codes, got {dtype}")
-    if dev < 0 or len(shape) != 4 or shape[3] != 64:
-        _refuse(k_cache, "k_cache", dtype, (None, None, None, 64), dev, strides=True)
-    if v_cache.dtype is not dtype or v_cache.get_device() != dev or v_cache.shape != shape:
-        _refuse(v_cache, "v_cache", dtype, tuple(shape), dev, strides=True)
-    if v_cache.stride() != st or st[3] != 1:
-        raise ValueError("k_cache and v_cache need the same strides, with contiguous rows")
-    if codes:
-        if k_scale is None or v_scale is None:
-            raise ValueError("an e4m3 cache needs k_scale and v_scale")
-        _check(k_scale, "k_scale", _F32, (shape[2],), dev)
-        _check(v_scale, "v_scale", _F32, (shape[2],), dev)
-    elif k_scale is not None or v_scale is not None:
-        raise ValueError("a bf16 cache takes no scales")
-    return codes, dev, shape, st
+def _on(stream, t):
+    """The context of a paged call on a given stream."""
+    if stream.device != t.device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors are on {t.device}")
+    return torch.cuda.stream(stream)
 
 
 def paged_plan(cached_lens, new_lens, block_table, free_pages, pool, page_size, max_tokens, window=0, first_page=None,
@@ -426,62 +375,19 @@ def paged_plan(cached_lens, new_lens, block_table, free_pages, pool, page_size, 
     block_table [B, max_pages] and free_pages [num_pages] (both updated in
     place), pool [2] = (head, count) of the ring of free pages, first_page [B]
     or None; all int32 CUDA.  Returns (cu_seqlens [B + 1], kv_lens [B],
-    slot_map [max_tokens], pool_out [2], first_page_out [B] or None); the ones
-    that are not given are parts of one new tensor.
+    slot_map [max_tokens], pool_out [2], first_page_out [B] or None).
     kv_lens, pool_out and first_page_out may be given as cached_lens, pool and
     first_page, which updates those in place."""
-    dev = cached_lens.get_device()
-    B = cached_lens.numel()
-    if dev < 0:
-        _refuse(cached_lens, "cached_lens", _I32, (B,), dev)
-    _check(cached_lens, "cached_lens", _I32, (B,), dev)
-    _check(new_lens, "new_lens", _I32, (B,), dev)
-    if block_table.dim() != 2:
-        _refuse(block_table, "block_table", _I32, (B, None), dev)
-    max_pages = block_table.shape[1]
-    _check(block_table, "block_table", _I32, (B, max_pages), dev)
-    pages = free_pages.numel()
-    _check(free_pages, "free_pages", _I32, (pages,), dev)
-    _check(pool, "pool", _I32, (2,), dev)
-    if first_page is not None:
-        _check(first_page, "first_page", _I32, (B,), dev)
-    elif window > 0 or first_page_out is not None:
-        raise ValueError("giving back a window's pages needs first_page")
-    max_tokens = int(max_tokens)
-    given = [cu_seqlens, kv_lens, slot_map, pool_out]
-    sizes = [B + 1, B, max_tokens, 2]
-    if first_page is not None:
-        given.append(first_page_out)
-        sizes.append(B)
-    for t, name, n in zip(given, ("cu_seqlens", "kv_lens", "slot_map", "pool_out", "first_page_out"), sizes):
-        if t is not None:
-            _check(t, name, _I32, (n,), dev)
-
-    def call(s):
-        new = [0 if t is not None else n for t, n in zip(given, sizes)]
-        if any(new):
-            parts = cached_lens.new_empty(sum(new)).split_with_sizes(new)
-            out = [p if t is None else t for t, p in zip(given, parts)]
-        else:
-            out = given
-        if first_page is None:
-            out = [*out, None]
-        if B == 0:
-            out[0].zero_()
-            out[2].fill_(-1)
-            out[3].copy_(pool)
-            return tuple(out)
-        dims = PlanDims(B, max_tokens, max_pages, int(page_size), pages)
-        st = load().sink_attn_paged_plan(
-            ctypes.byref(dims), cached_lens.data_ptr(), new_lens.data_ptr(), block_table.data_ptr(),
-            free_pages.data_ptr(), pool.data_ptr(), None if first_page is None else first_page.data_ptr(), int(window),
-            out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr(), out[3].data_ptr(),
-            None if first_page is None else out[4].data_ptr(), s)
-        if st != 0:
-            raise SinkAttnError(st, "sink_attn_paged_plan")
-        return tuple(out)
-
-    return _on_stream(call, dev, stream)
+    args = (cached_lens, new_lens, block_table, free_pages, pool, page_size, max_tokens, window, first_page,
+            cu_seqlens, kv_lens, slot_map, pool_out, first_page_out)
+    if stream is None:
+        r = (_paged or _paged_calls()).plan(*args)
+    else:
+        with _on(stream, cached_lens):
+            r = _paged_calls().plan(*args)
+    if type(r) is int:
+        raise SinkAttnError(r, "sink_attn_paged_plan")
+    return r
 
 
 def paged_append(k_new, v_new, slot_map, k_cache, v_cache, k_scale=None, v_scale=None, *, stream=None):
@@ -490,33 +396,15 @@ def paged_append(k_new, v_new, slot_map, k_cache, v_cache, k_scale=None, v_scale
     [T, Hkv, D] bf16, at any token stride; slot_map int32 [T], negative slots
     are skipped; k_cache / v_cache [num_pages, page_size, Hkv, D], updated in
     place.  Returns (k_cache, v_cache)."""
-    codes, dev, (pages, page, hkv, _), st_ = _paged_cache(k_cache, v_cache, k_scale, v_scale)
-    T = k_new.shape[0]
-    ks, vs = _check_heads(k_new, "k_new", hkv, dev), _check_heads(v_new, "v_new", hkv, dev)
-    if v_new.shape[0] != T:
-        _refuse(v_new, "v_new", _BF16, (T, hkv, 64), dev, strides=True)
-    _check(slot_map, "slot_map", _I32, (T,), dev)
-
-    def call(s):
-        dims = PagedDims(0, T, 0, 0, hkv, 64, page, pages, 0, st_[0], st_[1], st_[2], 0)
-        args = (ctypes.byref(dims), k_new.data_ptr(), v_new.data_ptr(), ks, vs, slot_map.data_ptr(),
-                k_cache.data_ptr(), v_cache.data_ptr())
-        if codes:
-            st = load().sink_attn_paged_append_e4m3(*args, k_scale.data_ptr(), v_scale.data_ptr(), s)
-        else:
-            st = load().sink_attn_paged_append(*args, s)
-        if st != 0:
-            raise SinkAttnError(st, "sink_attn_paged_append_e4m3" if codes else "sink_attn_paged_append")
-        return k_cache, v_cache
-
-    return _on_stream(call, dev, stream)
-
-
-@functools.lru_cache(maxsize=1024)
-def _paged_dims(*sizes):
-    """A call's sizes as the C structure, and the workspace they need."""
-    dims = ctypes.byref(PagedDims(*sizes))
-    return dims, int(load().sink_attn_paged_workspace_size(dims))
+    args = (k_new, v_new, slot_map, k_cache, v_cache, k_scale, v_scale)
+    if stream is None:
+        r = (_paged or _paged_calls()).append(*args)
+    else:
+        with _on(stream, k_cache):
+            r = _paged_calls().append(*args)
+    if type(r) is int:
+        raise SinkAttnError(r, "sink_attn_paged_append" if k_scale is None else "sink_attn_paged_append_e4m3")
+    return r
 
 
 def paged_attn(q, k_cache, v_cache, block_table, cu_seqlens, kv_lens, sinks, window=0, scale=None, *, max_new=None,
@@ -529,43 +417,16 @@ def paged_attn(q, k_cache, v_cache, block_table, cu_seqlens, kv_lens, sinks, win
     [Hq] fp32.  max_new bounds the new tokens of one request (default T).
     Returns (out [T, Hq, D], lse [Hq, T]); rows behind cu_seqlens[B] are left
     as they were."""
-    codes, dev, (pages, page, hkv, _), st_ = _paged_cache(k_cache, v_cache, k_scale, v_scale)
-    T, Hq = q.shape[0], q.shape[1]
-    B = kv_lens.numel()
-    qs = _check_heads(q, "q", Hq, dev)
-    if block_table.dim() != 2:
-        _refuse(block_table, "block_table", _I32, (B, None), dev)
-    max_pages = block_table.shape[1]
-    _check(block_table, "block_table", _I32, (B, max_pages), dev)
-    _check(cu_seqlens, "cu_seqlens", _I32, (B + 1,), dev)
-    _check(kv_lens, "kv_lens", _I32, (B,), dev)
-    _check(sinks, "sinks", _F32, (Hq,), dev)
-    if out is not None:
-        _check(out, "out", _BF16, (T, Hq, 64), dev)
-    if lse is not None:
-        _check(lse, "lse", _F32, (Hq, T), dev)
-    if workspace is not None and (workspace.get_device() != dev or not workspace.is_contiguous()):
-        raise ValueError(f"workspace: expected a contiguous tensor on cuda:{dev}, got one on {workspace.device}")
-    dims, need = _paged_dims(B, T, int(max(T, 1) if max_new is None else max_new), Hq, hkv, 64, page, pages, max_pages,
-                             st_[0], st_[1], st_[2], qs)
-
-    def call(s):
-        y = q.new_empty((T, Hq, 64)) if out is None else out
-        z = sinks.new_empty((Hq, T)) if lse is None else lse
-        w = sinks.new_empty((need >> 2) + 1) if workspace is None else workspace
-        args = (dims, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
-                cu_seqlens.data_ptr(), kv_lens.data_ptr())
-        tail = (sinks.data_ptr(), int(window), 0.125 if scale is None else float(scale), y.data_ptr(), z.data_ptr(),
-                w.data_ptr(), w.nbytes, s)
-        if codes:
-            st = load().sink_attn_paged_attn_e4m3(*args, k_scale.data_ptr(), v_scale.data_ptr(), *tail)
-        else:
-            st = load().sink_attn_paged_attn(*args, *tail)
-        if st != 0:
-            raise SinkAttnError(st, "sink_attn_paged_attn_e4m3" if codes else "sink_attn_paged_attn")
-        return y, z
-
-    return _on_stream(call, dev, stream)
+    args = (q, k_cache, v_cache, block_table, cu_seqlens, kv_lens, sinks, window, scale, max_new, k_scale, v_scale, out,
+            lse, workspace)
+    if stream is None:
+        r = (_paged or _paged_calls()).attn(*args)
+    else:
+        with _on(stream, k_cache):
+            r = _paged_calls().attn(*args)
+    if type(r) is int:
+        raise SinkAttnError(r, "sink_attn_paged_attn" if k_scale is None else "sink_attn_paged_attn_e4m3")
+    return r
 
 
 def device_error(stream=None) -> int:
