@@ -25,13 +25,14 @@ struct PagedParams {
   const float* sinks;
   __nv_bfloat16* out;
   float* lse;
-  // The few-rows kernel: key/value heads in chunks, and its workspace, per
-  // worker two partial results for each head of a chunk (unnormalised O,
-  // reference max, sum), the cut request (and chunk) that its piece completes,
-  // and whether a request that it does not complete begins in its piece.
-  int chunks, per_chunk;
-  float* part_o;     // [workers][2][per_chunk][kR][64]
-  float2* part_ml;   // [workers][2][per_chunk][kR] (m in log2 units, l)
+  // The few-rows kernel: chunks of key/value heads, heads of a chunk and warps
+  // that share a head's rows; and its workspace, per worker two partial results
+  // for each of its warps (unnormalised O, reference max, sum), the cut request
+  // (and chunk) that its piece completes, and whether a request that it does
+  // not complete begins in its piece.
+  int chunks, per_chunk, row_parts;
+  float* part_o;     // [workers][2][warps of a worker][kR][64]
+  float2* part_ml;   // [workers][2][warps of a worker][kR] (m in log2 units, l)
   int4* part_unit;   // [workers] (b or -1, chunk, begins, 0)
 };
 

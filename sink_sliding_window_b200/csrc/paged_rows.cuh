@@ -15,8 +15,11 @@
 // requests of 6-8k took 219 us; with every warp fetching its own head's boxes
 // the issue took 570 of a block's 1650 cycles, 900 of 2700 for e4m3.)
 // A warp keeps running maximum, sum and O of its head's n * G query rows (n
-// new tokens, G heads; one or two 16-row MMA tiles) in registers, and shares
-// nothing with the others.  The tiles come to the tensor cores through
+// new tokens, G heads; one 16-row MMA tile) in registers; with more rows two
+// to four warps share a head's ring, 16 rows each, and a worker has fewer
+// heads (one warp with two tiles spilled, and took 24 us for 16 requests of
+// 1000 keys and four tokens; two warps take 16).  Else warps share nothing.
+// The tiles come to the tensor cores through
 // mma.sync: with 8 or 16 rows the S and P of a block are a few registers, and
 // the trip through tensor memory that the 128-row instructions need costs more
 // than the multiplication (the decode kernel over linear caches makes that
@@ -46,25 +49,26 @@ namespace sa {
 
 template <bool kF8>
 constexpr int kRowsKeys = kF8 ? 64 : 32;  // keys of a block: 4 KB of K, 4 KB of V for each head
-constexpr int kRowsStages = 3;
-constexpr int kRowsMaxRows = 32;
-constexpr int kRowsHeads = 8;  // key/value heads of a chunk, at most
+constexpr int kRowsStages = 3;   // of the ring when every warp has a head of its own
+constexpr int kRowsMaxStages = 4 * kRowsStages;
+constexpr int kRowsMaxRows = 64;  // four warps of 16 rows share a head's ring
 // A cut closer than this many blocks to a request's end moves there: joining a
 // piece costs more than reading so few keys.
 template <bool kF8>
 constexpr int kRowsSnap = kF8 ? 1 : 2;
-// Fewest blocks of a worker.
+// Fewest blocks of a worker: a piece costs its join more than these few blocks
+// cost in a row (one request of 4033 keys: 16.1 us with 2, 12.9 with 4, 13.7 with 6).
 constexpr int kRowsMinBlocks = 4;
 constexpr int kRowsWarps = 8;  // that compute, of the one CTA of an SM
-constexpr int kRowsThreads = 32 * (kRowsWarps + 1);
+constexpr int kRowsThreads = 32 * (kRowsWarps + 1);  // the last warp copies
 constexpr int kRowsTile = 4096;  // bytes of one head's K or V block
 
 struct RowsCtl {
-  uint64_t full[kRowsWarps][kRowsStages];   // [worker of the CTA][stage]
-  uint64_t empty[kRowsWarps][kRowsStages];
+  uint64_t full[kRowsWarps * kRowsMaxStages];   // [worker of the CTA][stage]
+  uint64_t empty[kRowsWarps * kRowsMaxStages];
   int abort;
   int sums[kRowsWarps + 1];
-  int4 cuts[kRowsWarps + 1];  // where the pieces of the CTA's workers begin, and the last one ends: x, b, c, off
+  int4 cuts[kRowsWarps][2];  // where the pieces of the CTA's workers begin and end: x, b, c, off
 };
 
 constexpr size_t rows_smem_bytes(int batch) {
@@ -114,7 +118,7 @@ struct RowsAt {
 };
 
 // The axis: request by request, and within it chunk by chunk of its heads (one
-// chunk when there are at most kRowsHeads).  Its functions are called by whole
+// chunk when a CTA's warps are enough for them).  Its functions are called by whole
 // warps.
 template <int kSnap>
 struct RowsAxis {
@@ -175,12 +179,9 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
   constexpr int kThreads = kRowsThreads;
   constexpr int kTile = kRowsTile;
   constexpr int kKeys = kRowsKeys<kF8>;
-  // Keys of one softmax step: all of a block where registers allow it.
-  constexpr int kStep = kF8 && kR <= 16 ? 64 : 32;
-  constexpr int kNT = kStep / 8;
+  constexpr int kNT = kKeys / 8;  // 8-key MMA tiles of a block
   constexpr int kRow = kF8 ? 64 : 128;         // bytes of a key row in shared memory
-  constexpr int kMT = kR == 32 ? 2 : 1;        // 16-row MMA tiles
-  constexpr int kHalves = kR == 8 ? 1 : 2;     // 8-row halves of a tile that hold rows
+  constexpr int kHalves = kR == 8 ? 1 : 2;     // 8-row halves of the MMA tile that hold rows
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align1024(smem_raw);
   RowsCtl* ctl = reinterpret_cast<RowsCtl*>(smem + kWarps * kRowsStages * 2 * kTile);
@@ -189,13 +190,14 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_launch_dependents();  // the combine kernel waits for this one's end by itself
 
-  const int groups = kWarps / p.per_chunk;  // workers of this CTA
+  const int per_group = p.per_chunk * p.row_parts;  // warps of a worker
+  const int groups = kWarps / per_group;             // workers of this CTA
+  const int stages = kRowsStages * p.row_parts;
   if (threadIdx.x == 0) {
-    for (int w = 0; w < groups; ++w)
-      for (int s = 0; s < kRowsStages; ++s) {
-        mbar_init(&ctl->full[w][s], 1);
-        mbar_init(&ctl->empty[w][s], p.per_chunk);
-      }
+    for (int w = 0; w < groups * stages; ++w) {
+      mbar_init(&ctl->full[w], 1);
+      mbar_init(&ctl->empty[w], per_group);
+    }
     ctl->abort = 0;
     fence_mbar_init();
     tma_prefetch_desc(&tm_k);
@@ -241,17 +243,20 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
   axis.total = static_cast<uint32_t>(pre[p.batch]) * p.chunks;
   axis.workers = min(gridDim.x * groups, (axis.total + kRowsMinBlocks - 1) / kRowsMinBlocks);
 
-  for (int g = warp; g <= groups; g += kWarps + 1) {
-    const RowsAt a = axis.cut(blockIdx.x * groups + g);
-    if (lane == 0) ctl->cuts[g] = make_int4(static_cast<int>(a.x), a.b, a.c, a.off);
+  // Worker g of this CTA: consecutive pieces go to different SMs, so that a few
+  // of them do not share one.
+  auto worker_of = [&](int g) { return blockIdx.x + gridDim.x * g; };
+  for (int i = warp; i < 2 * groups; i += kWarps + 1) {
+    const RowsAt a = axis.cut(worker_of(i >> 1) + (i & 1));
+    if (lane == 0) ctl->cuts[i >> 1][i & 1] = make_int4(static_cast<int>(a.x), a.b, a.c, a.off);
   }
   __syncthreads();
-  auto cut_of = [&](int g) {
-    const int4 v = ctl->cuts[g];
+  auto cut_of = [&](int g, int end) {
+    const int4 v = ctl->cuts[g][end];
     return RowsAt{static_cast<uint32_t>(v.x), v.y, v.z, v.w};
   };
 
-  const uint32_t group_bytes = p.per_chunk * kRowsStages * 2 * kTile, stage_bytes = p.per_chunk * 2 * kTile;
+  const uint32_t group_bytes = p.per_chunk * stages * 2 * kTile, stage_bytes = p.per_chunk * 2 * kTile;
   if (warp == kWarps) {
     // ------------------------------------------------------------------ copies
     // Lanes lpg * g .. of the warp keep the state of worker g and, one per
@@ -259,8 +264,8 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
     // is looked up while this one is copied.
     const int nbox_log2 = (kF8 ? 6 : 5) - p.box_log2, nbox = 1 << nbox_log2, lpg = 32 / groups;
     const int mine = min(lane / lpg, groups - 1), li = lane - mine * lpg;
-    RowsAt at = cut_of(mine);
-    const int count = static_cast<int>(cut_of(mine + 1).x - at.x);
+    RowsAt at = cut_of(mine, 0);
+    const int count = static_cast<int>(cut_of(mine, 1).x - at.x);
     int left = count;
     struct Batch {
       int n, c, key, entry;  // blocks, chunk, first key, this lane's table entry
@@ -286,8 +291,8 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
     int j = 0, page = now.want ? paged_page(p, now.entry) : p.num_pages;
     const int most = __reduce_max_sync(0xffffffffu, count);
     bool ok = true;
+    int s = 0, turn = 0;  // i = turn * stages + s
     for (int i = 0; ok && i < most; ++i) {
-      const int s = i % kRowsStages;
       if (j == now.n) {
         now = next;
         page = now.want ? paged_page(p, now.entry) : p.num_pages;
@@ -304,11 +309,11 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
 #pragma unroll
         for (int x = 0; x < kKeys / 16; ++x) pages[x] = __shfl_sync(0xffffffffu, page, src + jg * nbox + min(x, nbox - 1));
         if (i >= __shfl_sync(0xffffffffu, count, src)) continue;
-        if (i >= kRowsStages)
-          ok = warp_all(mbar_wait(&ctl->empty[g][s], ((i / kRowsStages) - 1) & 1, abort, &g_device_error,
+        if (turn > 0)
+          ok = warp_all(mbar_wait(&ctl->empty[g * stages + s], (turn - 1) & 1, abort, &g_device_error,
                                   kDevErrTimeoutProducer));
         if (ok && elect_one()) {
-          uint64_t* full = &ctl->full[g][s];
+          uint64_t* full = &ctl->full[g * stages + s];
           uint8_t* dst = smem + g * group_bytes + s * stage_bytes;
           mbar_arrive_expect_tx(full, stage_bytes);
 #pragma unroll
@@ -323,18 +328,20 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
         __syncwarp();
       }
       ++j;
+      if (++s == stages) s = 0, ++turn;
     }
     return;
   }
 
   // ----------------------------------------------------------------- attention
-  if (warp >= groups * p.per_chunk) return;
-  const int group = warp / p.per_chunk, hw = warp - group * p.per_chunk;  // worker of the CTA, head of its chunk
-  const int worker = blockIdx.x * groups + group;
-  const bool reports = p.part_unit && hw == 0 && lane == 0;
+  if (warp >= groups * per_group) return;
+  const int group = warp / per_group, in_group = warp - group * per_group;  // worker of the CTA, warp of the worker
+  const int hw = in_group / p.row_parts, row0 = 16 * (in_group - hw * p.row_parts);  // head of the chunk, first row
+  const int worker = worker_of(group);
+  const bool reports = p.part_unit && in_group == 0 && lane == 0;
   int4 unit = make_int4(-1, 0, 0, 0);  // see PagedParams::part_unit
-  RowsAt at = cut_of(group);
-  const int count = static_cast<int>(cut_of(group + 1).x - at.x);
+  RowsAt at = cut_of(group, 0);
+  const int count = static_cast<int>(cut_of(group, 1).x - at.x);
   if (count == 0) {
     if (reports) p.part_unit[worker] = unit;
     return;
@@ -342,15 +349,15 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
   PagedRequest rq = paged_request(p, at.b);
   int first = rows_first(p, rq), blocks = axis.blocks(at.b);
   const uint8_t* ring = smem + group * group_bytes;
-  uint64_t* full = ctl->full[group];
+  uint64_t *full = ctl->full + group * stages, *empty = ctl->empty + group * stages;
   // Keys of this warp's head within a box, and the bytes from one box to the next.
   const int box = 1 << p.box_log2, box_bytes = p.per_chunk * box * kRow;
   const int head_bytes = hw * box * kRow;
 
   const int t4 = lane & 3, r8 = lane >> 2;
-  uint32_t q[kMT][4][4];
-  float o[kMT][8][4], m[kMT][2], l[kMT][2];
-  int key_lo[kMT][2], key_hi[kMT][2];  // keys that this thread's rows see
+  uint32_t q[4][4];
+  float o[8][4], m[2], l[2];
+  int key_lo[2], key_hi[2];  // keys that this thread's rows see
   bool seg_begin = true, whole = false;
   // The last chunk may have fewer heads: a warp without one computes on zeros
   // and writes nothing.
@@ -358,7 +365,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
   int g = 0;
   float sl2 = 0.f;
   bool ok = true;
-  int done = 0;
+  int done = 0, s = 0, turn = 0;
 
   for (int i = 0; i < count; ++i) {
     if (seg_begin) {
@@ -368,43 +375,39 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
       real = at.c * p.per_chunk + hw < p.Hkv;
       sl2 = kF8 ? p.scale_log2 * __ldg(p.k_scale + g) : p.scale_log2;
 #pragma unroll
-      for (int mt = 0; mt < kMT; ++mt) {
+      for (int h = 0; h < 2; ++h) {
+        m[h] = -INFINITY;
+        l[h] = 0.f;
+        const int row = row0 + 8 * h + r8;
+        const int t = row / p.G;
+        key_hi[h] = t < rq.n ? rq.len - rq.n + t : -1;
+        key_lo[h] = p.window > 0 ? key_hi[h] - p.window + 1 : 0;
+        const __nv_bfloat16* src =
+            p.q + static_cast<long long>(rq.t0 + t) * p.q_stride + (g * p.G + row - t * p.G) * kHeadDim;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          m[mt][h] = -INFINITY;
-          l[mt][h] = 0.f;
-          const int row = 16 * mt + 8 * h + r8;
-          const int t = row / p.G;
-          key_hi[mt][h] = t < rq.n ? rq.len - rq.n + t : -1;
-          key_lo[mt][h] = p.window > 0 ? key_hi[mt][h] - p.window + 1 : 0;
-          const __nv_bfloat16* src =
-              p.q + static_cast<long long>(rq.t0 + t) * p.q_stride + (g * p.G + row - t * p.G) * kHeadDim;
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk) {
-            uint32_t a = 0u, c = 0u;
-            if (h < kHalves && t < rq.n) {
-              if constexpr (kF8) {
-                const uint2 v = __ldg(reinterpret_cast<const uint2*>(src + 16 * kk + 4 * t4));
-                a = bf16x2_to_f16x2_sat(v.x);
-                c = bf16x2_to_f16x2_sat(v.y);
-              } else {
-                a = __ldg(reinterpret_cast<const uint32_t*>(src + 16 * kk + 2 * t4));
-                c = __ldg(reinterpret_cast<const uint32_t*>(src + 16 * kk + 8 + 2 * t4));
-              }
+        for (int kk = 0; kk < 4; ++kk) {
+          uint32_t a = 0u, c = 0u;
+          if (h < kHalves && t < rq.n) {
+            if constexpr (kF8) {
+              const uint2 v = __ldg(reinterpret_cast<const uint2*>(src + 16 * kk + 4 * t4));
+              a = bf16x2_to_f16x2_sat(v.x);
+              c = bf16x2_to_f16x2_sat(v.y);
+            } else {
+              a = __ldg(reinterpret_cast<const uint32_t*>(src + 16 * kk + 2 * t4));
+              c = __ldg(reinterpret_cast<const uint32_t*>(src + 16 * kk + 8 + 2 * t4));
             }
-            q[mt][kk][h] = a;
-            q[mt][kk][2 + h] = c;
           }
+          q[kk][h] = a;
+          q[kk][2 + h] = c;
         }
-#pragma unroll
-        for (int n = 0; n < 8; ++n)
-#pragma unroll
-          for (int u = 0; u < 4; ++u) o[mt][n][u] = 0.f;
       }
+#pragma unroll
+      for (int n = 0; n < 8; ++n)
+#pragma unroll
+        for (int u = 0; u < 4; ++u) o[n][u] = 0.f;
     }
-    const int s = i % kRowsStages;
     done = i;
-    ok = warp_all(mbar_wait(&full[s], (i / kRowsStages) & 1, abort, &g_device_error, kDevErrTimeoutDecode));
+    ok = warp_all(mbar_wait(&full[s], turn & 1, abort, &g_device_error, kDevErrTimeoutDecode));
     if (!ok) break;
     const uint8_t* tile = ring + s * stage_bytes;
     const int base = first + at.off * kKeys;
@@ -430,175 +433,157 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
     // Where 16 keys of this warp's K lie: in a box of their own, or in one with others.
     auto keys16 = [&](int k) -> uint32_t { return ((16 * k) >> p.box_log2) * box_bytes + ((16 * k) & (box - 1)) * kRow; };
 
+    float x[kNT][4];
 #pragma unroll
-    for (int step = 0; step < kKeys / kStep; ++step) {
-      float x[kMT][kNT][4];
+    for (int nt = 0; nt < kNT; ++nt) {
+#pragma unroll
+      for (int u = 0; u < 4; ++u) x[nt][u] = 0.f;
+      const int r = 8 * (nt & 1) + (lane & 7), ch = lane >> 3;
+      const uint32_t sk16 = sk + keys16(nt >> 1) + r * kRow;
+      if constexpr (kF8) {
+        uint32_t k[4];
+        ldsm4(sk16 + ((ch ^ ((r >> 1) & 3)) << 4), k);
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          mma_16816<true>(x[nt], q[kk], e4m3x2_to_f16x2(k[kk]), e4m3x2_to_f16x2(k[kk] >> 16));
+      } else {
+        uint32_t k[8];
+        ldsm4(sk16 + ((ch ^ (r & 7)) << 4), k);
+        ldsm4(sk16 + (((ch + 4) ^ (r & 7)) << 4), k + 4);
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          mma_16816<false>(x[nt], q[kk], k[2 * kk], k[2 * kk + 1]);
+      }
+    }
+    if (masked) {
+      const int j0 = base + 2 * t4;
+#pragma unroll
+      for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+        for (int u = 0; u < 2 * kHalves; ++u) {
+          const int j = j0 + 8 * nt + (u & 1);
+          if (j < key_lo[u >> 1] || j > key_hi[u >> 1]) x[nt][u] = -INFINITY;
+        }
+    }
+    uint32_t pk[kNT][2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if (h >= kHalves) {
+#pragma unroll
+        for (int nt = 0; nt < kNT; ++nt) pk[nt][h] = 0u;
+        continue;
+      }
+      float top = -INFINITY;
+#pragma unroll
+      for (int nt = 0; nt < kNT; ++nt) top = fmax3(top, x[nt][2 * h], x[nt][2 * h + 1]);
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2)) * sl2;
+      const float old = m[h];
+      if (__any_sync(0xffffffffu, top > old)) {
+        const float now = fmaxf(old, top);
+        const float f = now == -INFINITY ? 1.f : ex2_approx(old - now);
+        m[h] = now;
+        l[h] *= f;
+#pragma unroll
+        for (int n = 0; n < 8; ++n) o[n][2 * h] *= f, o[n][2 * h + 1] *= f;
+      }
+      const float ref = m[h] == -INFINITY ? 0.f : m[h];
+      float sum = 0.f;
 #pragma unroll
       for (int nt = 0; nt < kNT; ++nt) {
+        const float e0 = ex2_approx(fmaf(x[nt][2 * h], sl2, -ref));
+        const float e1 = ex2_approx(fmaf(x[nt][2 * h + 1], sl2, -ref));
+        sum += e0 + e1;
+        pk[nt][h] = kF8 ? pack_f16x2(e0, e1) : pack_bf16x2(e0, e1);
+      }
+      l[h] += sum;
+    }
 #pragma unroll
-        for (int mt = 0; mt < kMT; ++mt)
+    for (int ks = 0; ks < kKeys / 16; ++ks) {
+      const int r = (lane & 7) + (lane & 8), ch = lane >> 4;
+      const uint32_t sv16 = sv + keys16(ks) + r * kRow;
 #pragma unroll
-          for (int u = 0; u < 4; ++u) x[mt][nt][u] = 0.f;
-        const int r = 8 * (nt & 1) + (lane & 7), ch = lane >> 3;
-        const uint32_t sk16 = sk + keys16(step * (kStep / 16) + (nt >> 1)) + r * kRow;
+      for (int j = 0; j < (kF8 ? 2 : 4); ++j) {
+        uint32_t v[4];
         if constexpr (kF8) {
-          uint32_t k[4];
-          ldsm4(sk16 + ((ch ^ ((r >> 1) & 3)) << 4), k);
+          ldsm4_t(sv16 + (((2 * j + ch) ^ ((r >> 1) & 3)) << 4), v);
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-#pragma unroll
-            for (int mt = 0; mt < kMT; ++mt)
-              mma_16816<true>(x[mt][nt], q[mt][kk], e4m3x2_to_f16x2(k[kk]), e4m3x2_to_f16x2(k[kk] >> 16));
+          for (int u = 0; u < 4; ++u) v[u] = __byte_perm(v[u], 0u, 0x3120);
         } else {
-          uint32_t k[8];
-          ldsm4(sk16 + ((ch ^ (r & 7)) << 4), k);
-          ldsm4(sk16 + (((ch + 4) ^ (r & 7)) << 4), k + 4);
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-#pragma unroll
-            for (int mt = 0; mt < kMT; ++mt) mma_16816<false>(x[mt][nt], q[mt][kk], k[2 * kk], k[2 * kk + 1]);
+          ldsm4_t(sv16 + (((2 * j + ch) ^ (r & 7)) << 4), v);
         }
-      }
-      if (masked) {
-        const int j0 = base + kStep * step + 2 * t4;
+        const uint32_t a[4] = {pk[2 * ks][0], pk[2 * ks][1], pk[2 * ks + 1][0], pk[2 * ks + 1][1]};
+        if constexpr (kF8) {
 #pragma unroll
-        for (int mt = 0; mt < kMT; ++mt)
-#pragma unroll
-          for (int nt = 0; nt < kNT; ++nt)
-#pragma unroll
-            for (int u = 0; u < 2 * kHalves; ++u) {
-              const int j = j0 + 8 * nt + (u & 1);
-              if (j < key_lo[mt][u >> 1] || j > key_hi[mt][u >> 1]) x[mt][nt][u] = -INFINITY;
-            }
-      }
-      uint32_t pk[kMT][kNT][2];
-#pragma unroll
-      for (int mt = 0; mt < kMT; ++mt) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (h >= kHalves) {
-#pragma unroll
-            for (int nt = 0; nt < kNT; ++nt) pk[mt][nt][h] = 0u;
-            continue;
+          for (int u = 0; u < 2; ++u) {  // 16 dims: the even ones, the odd ones
+            mma_16816<true>(o[2 * (2 * j + u)], a, e4m3x2_to_f16x2(v[2 * u]), e4m3x2_to_f16x2(v[2 * u + 1]));
+            mma_16816<true>(o[2 * (2 * j + u) + 1], a, e4m3x2_to_f16x2(v[2 * u] >> 16),
+                            e4m3x2_to_f16x2(v[2 * u + 1] >> 16));
           }
-          float top = -INFINITY;
-#pragma unroll
-          for (int nt = 0; nt < kNT; ++nt) top = fmax3(top, x[mt][nt][2 * h], x[mt][nt][2 * h + 1]);
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2)) * sl2;
-          const float old = m[mt][h];
-          if (__any_sync(0xffffffffu, top > old)) {
-            const float now = fmaxf(old, top);
-            const float f = now == -INFINITY ? 1.f : ex2_approx(old - now);
-            m[mt][h] = now;
-            l[mt][h] *= f;
-#pragma unroll
-            for (int n = 0; n < 8; ++n) o[mt][n][2 * h] *= f, o[mt][n][2 * h + 1] *= f;
-          }
-          const float ref = m[mt][h] == -INFINITY ? 0.f : m[mt][h];
-          float sum = 0.f;
-#pragma unroll
-          for (int nt = 0; nt < kNT; ++nt) {
-            const float e0 = ex2_approx(fmaf(x[mt][nt][2 * h], sl2, -ref));
-            const float e1 = ex2_approx(fmaf(x[mt][nt][2 * h + 1], sl2, -ref));
-            sum += e0 + e1;
-            pk[mt][nt][h] = kF8 ? pack_f16x2(e0, e1) : pack_bf16x2(e0, e1);
-          }
-          l[mt][h] += sum;
-        }
-      }
-#pragma unroll
-      for (int ks = 0; ks < kStep / 16; ++ks) {
-        const int r = (lane & 7) + (lane & 8), ch = lane >> 4;
-        const uint32_t sv16 = sv + keys16(step * (kStep / 16) + ks) + r * kRow;
-#pragma unroll
-        for (int j = 0; j < (kF8 ? 2 : 4); ++j) {
-          uint32_t v[4];
-          if constexpr (kF8) {
-            ldsm4_t(sv16 + (((2 * j + ch) ^ ((r >> 1) & 3)) << 4), v);
-#pragma unroll
-            for (int u = 0; u < 4; ++u) v[u] = __byte_perm(v[u], 0u, 0x3120);
-          } else {
-            ldsm4_t(sv16 + (((2 * j + ch) ^ (r & 7)) << 4), v);
-          }
-#pragma unroll
-          for (int mt = 0; mt < kMT; ++mt) {
-            const uint32_t a[4] = {pk[mt][2 * ks][0], pk[mt][2 * ks][1], pk[mt][2 * ks + 1][0], pk[mt][2 * ks + 1][1]};
-            if constexpr (kF8) {
-#pragma unroll
-              for (int u = 0; u < 2; ++u) {  // 16 dims: the even ones, the odd ones
-                mma_16816<true>(o[mt][2 * (2 * j + u)], a, e4m3x2_to_f16x2(v[2 * u]), e4m3x2_to_f16x2(v[2 * u + 1]));
-                mma_16816<true>(o[mt][2 * (2 * j + u) + 1], a, e4m3x2_to_f16x2(v[2 * u] >> 16),
-                                e4m3x2_to_f16x2(v[2 * u + 1] >> 16));
-              }
-            } else {
-              mma_16816<false>(o[mt][2 * j], a, v[0], v[1]);
-              mma_16816<false>(o[mt][2 * j + 1], a, v[2], v[3]);
-            }
-          }
+        } else {
+          mma_16816<false>(o[2 * j], a, v[0], v[1]);
+          mma_16816<false>(o[2 * j + 1], a, v[2], v[3]);
         }
       }
     }
     // This warp has read the stage, before the copy that reuses it.
     fence_proxy_async_smem();
     __syncwarp();
-    if (lane == 0) mbar_arrive(&ctl->empty[group][s]);
+    if (lane == 0) mbar_arrive(&empty[s]);
+    if (++s == stages) s = 0, ++turn;
 
     const bool unit_end = at.off + 1 == blocks;
     if (unit_end || i + 1 == count) {
       // ------------------------------------------- end of this piece of the request
       const bool begun = whole;
       whole = whole && unit_end;
-      const int slot = (2 * worker + (unit_end ? 0 : 1)) * p.per_chunk + hw;
+      const int slot = (2 * worker + (unit_end ? 0 : 1)) * per_group + in_group;
       const float vs = kF8 ? __ldg(p.v_scale + g) : 1.f;
 #pragma unroll
-      for (int mt = 0; mt < kMT; ++mt) {
-#pragma unroll
-        for (int h = 0; h < kHalves; ++h) {
-          const int row = 16 * mt + 8 * h + r8;
-          float sum = l[mt][h];
-          sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-          sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-          const int t = row / p.G;
-          const bool valid = t < rq.n && real;
-          const int head = valid ? g * p.G + row - t * p.G : 0;
-          float f = vs;
-          if (whole) {
-            const float s2 = __ldg(p.sinks + head) * kLog2e;
-            const float top = fmaxf(s2, m[mt][h]);
-            float all = 0.f;
-            f = 0.f;
-            if (top != -INFINITY) {
-              f = ex2_approx(m[mt][h] - top);
-              all = fmaf(sum, f, s2 == top ? 1.f : ex2_approx(s2 - top));
-              f = all > 0.f ? vs * f / all : 0.f;
-            }
-            if (valid && t4 == 0)
-              p.lse[static_cast<long long>(head) * p.T + rq.t0 + t] = all > 0.f ? (top + __log2f(all)) * kLn2 : -INFINITY;
-          } else if (valid && t4 == 0) {
-            p.part_ml[slot * kR + row] = make_float2(m[mt][h], sum);
+      for (int h = 0; h < kHalves; ++h) {
+        const int row = row0 + 8 * h + r8;
+        float sum = l[h];
+        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+        const int t = row / p.G;
+        const bool valid = t < rq.n && real;
+        const int head = valid ? g * p.G + row - t * p.G : 0;
+        float f = vs;
+        if (whole) {
+          const float s2 = __ldg(p.sinks + head) * kLog2e;
+          const float top = fmaxf(s2, m[h]);
+          float all = 0.f;
+          f = 0.f;
+          if (top != -INFINITY) {
+            f = ex2_approx(m[h] - top);
+            all = fmaf(sum, f, s2 == top ? 1.f : ex2_approx(s2 - top));
+            f = all > 0.f ? vs * f / all : 0.f;
           }
-          if (!valid) continue;
-          __nv_bfloat16* dst = p.out + (static_cast<long long>(rq.t0 + t) * p.Hq + head) * kHeadDim;
-          float* part = p.part_o + (static_cast<long long>(slot) * kR + row) * kHeadDim;
+          if (valid && t4 == 0)
+            p.lse[static_cast<long long>(head) * p.T + rq.t0 + t] = all > 0.f ? (top + __log2f(all)) * kLn2 : -INFINITY;
+        } else if (valid && t4 == 0) {
+          p.part_ml[slot * kR + row - row0] = make_float2(m[h], sum);
+        }
+        if (!valid) continue;
+        __nv_bfloat16* dst = p.out + (static_cast<long long>(rq.t0 + t) * p.Hq + head) * kHeadDim;
+        float* part = p.part_o + (static_cast<long long>(slot) * kR + row - row0) * kHeadDim;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            // 16 dims: two MMA tiles, side by side (bf16) or even and odd dims (e4m3).
-            const float y0 = o[mt][2 * e][2 * h] * f, y1 = o[mt][2 * e][2 * h + 1] * f;
-            const float z0 = o[mt][2 * e + 1][2 * h] * f, z1 = o[mt][2 * e + 1][2 * h + 1] * f;
-            if constexpr (kF8) {
-              const int d = 16 * e + 4 * t4;
-              if (whole) *reinterpret_cast<uint2*>(dst + d) = make_uint2(pack_bf16x2(y0, z0), pack_bf16x2(y1, z1));
-              else *reinterpret_cast<float4*>(part + d) = make_float4(y0, z0, y1, z1);
+        for (int e = 0; e < 4; ++e) {
+          // 16 dims: two MMA tiles, side by side (bf16) or even and odd dims (e4m3).
+          const float y0 = o[2 * e][2 * h] * f, y1 = o[2 * e][2 * h + 1] * f;
+          const float z0 = o[2 * e + 1][2 * h] * f, z1 = o[2 * e + 1][2 * h + 1] * f;
+          if constexpr (kF8) {
+            const int d = 16 * e + 4 * t4;
+            if (whole) *reinterpret_cast<uint2*>(dst + d) = make_uint2(pack_bf16x2(y0, z0), pack_bf16x2(y1, z1));
+            else *reinterpret_cast<float4*>(part + d) = make_float4(y0, z0, y1, z1);
+          } else {
+            const int d = 16 * e + 2 * t4;
+            if (whole) {
+              *reinterpret_cast<uint32_t*>(dst + d) = pack_bf16x2(y0, y1);
+              *reinterpret_cast<uint32_t*>(dst + d + 8) = pack_bf16x2(z0, z1);
             } else {
-              const int d = 16 * e + 2 * t4;
-              if (whole) {
-                *reinterpret_cast<uint32_t*>(dst + d) = pack_bf16x2(y0, y1);
-                *reinterpret_cast<uint32_t*>(dst + d + 8) = pack_bf16x2(z0, z1);
-              } else {
-                *reinterpret_cast<float2*>(part + d) = make_float2(y0, y1);
-                *reinterpret_cast<float2*>(part + d + 8) = make_float2(z0, z1);
-              }
+              *reinterpret_cast<float2*>(part + d) = make_float2(y0, y1);
+              *reinterpret_cast<float2*>(part + d + 8) = make_float2(z0, z1);
             }
           }
         }
@@ -624,9 +609,9 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
   if (!ok) {
     unit = make_int4(-1, 0, 0, 0);
     // Copies in flight still write to this CTA's shared memory.
-    for (int i = done; i < min(count, done + kRowsStages); ++i) {
+    for (int i = done; i < min(count, done + stages); ++i) {
       const uint64_t t0 = global_timer_ns();
-      while (!mbar_try_wait(&full[i % kRowsStages], (i / kRowsStages) & 1) && global_timer_ns() - t0 < kWaitLimitNs / 4) {
+      while (!mbar_try_wait(&full[i % stages], (i / stages) & 1) && global_timer_ns() - t0 < kWaitLimitNs / 4) {
       }
     }
   }
@@ -635,34 +620,40 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
 
 // Joins the pieces of every cut request and adds the sink: with M = max(s, max_k m_k),
 //   l = e^{s-M} + sum_k l_k e^{m_k-M},  out = sum_k O_k e^{m_k-M} / l,  lse = M + ln l.
-// One CTA per worker and head of a chunk, whose work is the request that the
+// One CTA per worker and warp of a worker, whose work is the request that the
 // worker completed (mostly none).  Its warps take the pieces in turn, eight
 // rows at a time (a lane holds four rows' four dims), then join their own
 // eight results in shared memory in the same way.
 template <int kR>
-__global__ void __launch_bounds__(256, 3) sink_attn_paged_join_kernel(const __grid_constant__ PagedParams p) {
+__global__ void __launch_bounds__(256, kR == 8 ? 3 : 2) sink_attn_paged_join_kernel(const __grid_constant__ PagedParams p) {
   __shared__ float s_o[8][8][kHeadDim];
   __shared__ float s_m[8][8], s_l[8][8];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_wait();
-  const int last = blockIdx.x, hw = blockIdx.y;
-  const int4 unit = __ldcg(p.part_unit + last);
-  const int g = unit.y * p.per_chunk + hw;
-  if (unit.x < 0 || g >= p.Hkv) return;
   // The first piece is that of the nearest worker before this one whose last
-  // piece begins a request.
-  const PagedRequest rq = paged_request(p, unit.x);
-  int start = last;
-  for (bool found = false; !found && start > 0;) {
+  // piece begins a request: one load per lane tells for 31 of them.
+  const int last = blockIdx.x, in_group = blockIdx.y, per_group = p.per_chunk * p.row_parts;
+  const int hw = in_group / p.row_parts, row0 = 16 * (in_group - hw * p.row_parts);
+  const int4 near = __ldcg(p.part_unit + max(last - lane, 0));
+  const int b = __shfl_sync(0xffffffffu, near.x, 0), g = __shfl_sync(0xffffffffu, near.y, 0) * p.per_chunk + hw;
+  if (b < 0 || g >= p.Hkv) return;
+  const PagedRequest rq = paged_request(p, b);
+  uint32_t begins = __ballot_sync(0xffffffffu, lane > 0 && lane <= last && near.z != 0);
+  int start = begins ? last - (__ffs(begins) - 1) : max(0, last - 31);
+  while (begins == 0 && start > 0) {
     const int w = start - 1 - lane;
-    const uint32_t begins = __ballot_sync(0xffffffffu, w >= 0 && __ldcg(&p.part_unit[max(w, 0)].z) != 0);
-    found = begins != 0;
-    start = found ? start - __ffs(begins) : max(0, start - 32);
+    begins = __ballot_sync(0xffffffffu, w >= 0 && __ldcg(&p.part_unit[max(w, 0)].z) != 0);
+    start = begins ? start - __ffs(begins) : max(0, start - 32);
   }
   const int pieces = last - start + 1;
-  auto slot = [&](int k) { return (k + 1 == pieces ? 2 * last : 2 * (start + k) + 1) * p.per_chunk + hw; };
-  const int rows = rq.n * p.G;
-  for (int r0 = 0; r0 < rows; r0 += 8) {
+  auto slot = [&](int k) { return (k + 1 == pieces ? 2 * last : 2 * (start + k) + 1) * per_group + in_group; };
+  // (The first loads wait for neither the request's lengths nor the sinks; a
+  // unit has a row at least.)
+  int r0 = 0;
+  do {
+    const int row = row0 + r0 + warp, t = row / p.G;  // this warp's row in the end
+    const int head = g * p.G + row - t * p.G;
+    const float s2 = __ldg(p.sinks + min(head, p.Hq - 1)) * kLog2e;
     // This lane's rows r0 + (lane >> 4) + 2 u, u < 4, and dims 4 (lane & 15) ..; a
     // piece's rows behind the last one are in the workspace, and never used.
     float m[4], l[4];
@@ -678,10 +669,9 @@ __global__ void __launch_bounds__(256, 3) sink_attn_paged_join_kernel(const __gr
         const int k = k0 + 8 * a;
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-          const int row = r0 + (lane >> 4) + 2 * u;
           ml[a][u] = make_float2(-INFINITY, 0.f);
-          if (k < pieces && row < rows) {
-            const long long at = static_cast<long long>(slot(k)) * kR + row;
+          if (k < pieces) {
+            const long long at = static_cast<long long>(slot(k)) * kR + r0 + (lane >> 4) + 2 * u;
             ml[a][u] = __ldcg(p.part_ml + at);
             v[a][u] = __ldcg(reinterpret_cast<const float4*>(p.part_o + at * kHeadDim) + (lane & 15));
           } else {
@@ -719,11 +709,7 @@ __global__ void __launch_bounds__(256, 3) sink_attn_paged_join_kernel(const __gr
     }
     __syncthreads();
     // One warp per row, two dims per lane.
-    const int row = r0 + warp;
-    if (row < rows) {
-      const int t = row / p.G;
-      const int head = g * p.G + row - t * p.G;
-      const float s2 = __ldg(p.sinks + head) * kLog2e;
+    if (t < rq.n) {
       float top = s2;
 #pragma unroll
       for (int w = 0; w < 8; ++w) top = fmaxf(top, s_m[w][warp]);
@@ -744,7 +730,8 @@ __global__ void __launch_bounds__(256, 3) sink_attn_paged_join_kernel(const __gr
       if (lane == 0)
         p.lse[static_cast<long long>(head) * p.T + rq.t0 + t] = all > 0.f ? (ref + __log2f(all)) * kLn2 : -INFINITY;
     }
-  }
+    r0 += 8;
+  } while (r0 < min(kR, rq.n * p.G - row0));
 }
 
 }  // namespace sa

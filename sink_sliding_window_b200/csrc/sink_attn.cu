@@ -652,7 +652,7 @@ sink_attn_status check_paged_attn(const sink_attn_paged_dims* d, bool codes) {
   // Positions are 32-bit, with room for a tile behind the last one; so are the
   // blocks of keys of all requests, and a worker's share of them.
   const int64_t tokens = static_cast<int64_t>(d->max_pages) * d->page_size;
-  const int64_t chunks = (d->num_kv_heads + kRowsHeads - 1) / kRowsHeads;
+  const int64_t chunks = d->num_kv_heads;  // of heads, at most
   if (tokens > (int64_t(1) << 30) || tokens * std::max(d->batch, 1) > (int64_t(1) << 35) / chunks)
     return SINK_ATTN_ERR_UNSUPPORTED;
   if (d->q_stride % 8) return SINK_ATTN_ERR_ALIGN;
@@ -660,10 +660,11 @@ sink_attn_status check_paged_attn(const sink_attn_paged_dims* d, bool codes) {
 }
 
 // Which kernels a call's requests go to.  A request of at most `few` new
-// tokens is the few-rows kernel's (kR rows: 8, 16 or 32, the smallest that
-// holds the call's requests if one does, else one token of a group).
+// tokens is the few-rows kernel's, with tiles of kR rows (8 or 16) and as many
+// warps a head as hold all of the call's requests, or if none do (the call has
+// chunks) one token of a group.
 struct PagedSplit {
-  int kR, few;
+  int kR, row_parts, few;
   bool rows, chunks;
 };
 
@@ -672,11 +673,18 @@ PagedSplit split_paged(const sink_attn_paged_dims* d) {
   const int G = d->num_q_heads / d->num_kv_heads;
   const int64_t need = static_cast<int64_t>(std::min(d->max_new, d->total_tokens)) * G;
   const int64_t fit = need <= kRowsMaxRows ? need : G;
-  s.kR = fit <= 8 ? 8 : fit <= 16 ? 16 : 32;
-  s.few = s.kR / G;
+  s.kR = fit <= 8 ? 8 : 16;
+  s.row_parts = fit <= 16 ? 1 : fit <= 32 ? 2 : 4;
+  s.few = std::min(kRowsMaxRows, s.kR * s.row_parts) / G;
   s.rows = s.few > 0;
   s.chunks = need > static_cast<int64_t>(s.few) * G;
   return s;
+}
+
+// Chunks of key/value heads of the few-rows kernel, and heads of a chunk.
+int rows_chunks(const sink_attn_paged_dims* d, const PagedSplit& s) {
+  const int heads = kRowsWarps / s.row_parts;
+  return (d->num_kv_heads + heads - 1) / heads;
 }
 
 constexpr int kPagedCtas = 148;  // one CTA per SM of a B200
@@ -796,18 +804,22 @@ bool launch_rows(PagedParams& p, const sink_attn_paged_dims* d, const void* k_ca
   if (!smem_set.ensure(sink_attn_paged_rows_kernel<kF8, kR>, rows_smem_bytes(kPagedMaxBatch))) return false;
   const bool join = !rows_never_cut<kF8>(p);
   if (!join) p.part_unit = nullptr;
-  sink_attn_paged_rows_kernel<kF8, kR><<<kPagedCtas, kRowsThreads, rows_smem_bytes(p.batch), st>>>(tm_k, tm_v, p);
+  // No more CTAs than the most blocks there can be give work to.
+  const int64_t keys = p.window > 0 ? static_cast<int64_t>(p.window) + p.few - 1 + box : INT64_MAX;
+  const int64_t most = (std::min(keys, int64_t(p.max_pages) << p.page_log2) + kRowsKeys<kF8> - 1) / kRowsKeys<kF8> + 1;
+  const int64_t workers = (most * p.batch * p.chunks + kRowsMinBlocks - 1) / kRowsMinBlocks;
+  const int per_group = p.per_chunk * p.row_parts, groups = kRowsWarps / per_group;
+  const int ctas = static_cast<int>(std::min<int64_t>(kPagedCtas, workers));
+  sink_attn_paged_rows_kernel<kF8, kR><<<ctas, kRowsThreads, rows_smem_bytes(p.batch), st>>>(tm_k, tm_v, p);
   if (cudaPeekAtLastError() != cudaSuccess) return false;
   if (!join) return true;
-  return launch_join(sink_attn_paged_join_kernel<kR>, dim3(kPagedCtas * (kRowsWarps / p.per_chunk), p.per_chunk), p, st);
+  return launch_join(sink_attn_paged_join_kernel<kR>, dim3(ctas * groups, per_group), p, st);
 }
 
 template <bool kF8>
 bool launch_rows(int kR, PagedParams& p, const sink_attn_paged_dims* d, const void* k_cache, const void* v_cache,
                  cudaStream_t st) {
-  return kR == 8    ? launch_rows<kF8, 8>(p, d, k_cache, v_cache, st)
-         : kR == 16 ? launch_rows<kF8, 16>(p, d, k_cache, v_cache, st)
-                    : launch_rows<kF8, 32>(p, d, k_cache, v_cache, st);
+  return kR == 8 ? launch_rows<kF8, 8>(p, d, k_cache, v_cache, st) : launch_rows<kF8, 16>(p, d, k_cache, v_cache, st);
 }
 
 // The query tile of the chunk kernel, `tokens` tokens of one group of heads.
@@ -879,7 +891,8 @@ sink_attn_status paged_attn_impl(const sink_attn_paged_dims* d, const void* q, c
   p.max_pages = d->max_pages;
   p.box_log2 = 0;
   p.few = split.few;
-  p.chunks = (p.Hkv + kRowsHeads - 1) / kRowsHeads;
+  p.row_parts = split.row_parts;
+  p.chunks = rows_chunks(d, split);
   p.per_chunk = (p.Hkv + p.chunks - 1) / p.chunks;
   p.window = window > 0 ? window : 0;
   p.scale_log2 = scale * kLog2e;
