@@ -7,8 +7,8 @@
 //
 // Work.  A unit is (request, kTiles tiles, key/value head).  The host knows
 // neither the lengths nor the number of units U; every CTA counts them for
-// itself (one pass over the lengths, a scan, no list in memory) and finds its
-// own, the longer units of a request first.  The CTAs that run at once make a
+// itself (one pass over the lengths, a scan, no list in memory) and takes one
+// of every wave, the longer units of a request first.  The CTAs that run at once make a
 // wave.  The units behind the last full wave are cut into k parts along their
 // keys, with k such that the parts fill whole waves as well as they can
 // (chunk_parts): a few rows over a long context take all SMs, and the last
@@ -63,6 +63,7 @@ struct ChunkParams {
 
 template <bool kF8>
 struct ChunkCtl {
+  // Barriers, q_full to o_full.
   uint64_t q_full;
   uint64_t q_conv;                 // e4m3: Q converted to fp16 in place (all softmax threads)
   uint64_t k_full[kFwdStages];     // e4m3: two arrivals, of the widening warps
@@ -75,7 +76,9 @@ struct ChunkCtl {
   uint64_t o_full;
   int units[kChunkThreads<kF8> / 32];  // sums per warp
   float steps[kChunkThreads<kF8> / 32];
-  int unit[2];                     // request, unit within it
+  int starts[kChunkThreads<kF8>];      // units before each thread's requests
+  int total, full, parts;              // units, those of full waves, parts of each of the others
+  int unit[2];                         // request, unit within it
   uint32_t tmem_base;
   int abort;
 };
@@ -165,13 +168,9 @@ __global__ void __launch_bounds__(kChunkThreads<kF8>, kChunkPerSm<kF8>)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_launch_dependents();
 
-  // ------------------------------------------------------- which unit, which part
-  int unit, part, parts, slot;
-  PagedRequest rq;
-  int b, group, g;
+  // -------------------------------------------------------- the units of the call
+  const int per = (p.a.batch + kThreads - 1) / kThreads, b0 = threadIdx.x * per;  // this thread's requests
   {
-    const int per = (p.a.batch + kThreads - 1) / kThreads;
-    const int b0 = threadIdx.x * per;
     int units = 0;
     float steps = 0.f;
     for (int i = 0; i < per && b0 + i < p.a.batch; ++i) {
@@ -184,376 +183,406 @@ __global__ void __launch_bounds__(kChunkThreads<kF8>, kChunkPerSm<kF8>)
     int upto, total;
     float all_steps;
     chunk_scan<kF8>(ctl, units, steps, upto, total, all_steps);
-    const int full = total / p.wave * p.wave, rest = total - full;
-    parts = p.part_o && rest ? chunk_parts(rest, static_cast<int>(all_steps / total), p.wave) : 1;
-    if (blockIdx.x == 0 && threadIdx.x == 0 && p.part_units) *p.part_units = parts > 1 ? rest : 0;
-    unit = blockIdx.x;
-    part = 0;
-    slot = 0;
-    if (unit >= full) {
-      slot = unit - full;
-      unit = full + slot / parts;
-      part = slot % parts;
-    } else {
-      parts = 1;
-    }
-    if (unit >= total) return;
-    int at = upto - units;
-    if (unit >= at && unit < upto) {
-      for (int i = 0;; ++i) {
-        const int n = chunk_units<kF8>(p, paged_request(p.a, b0 + i)) * p.a.Hkv;
-        if (unit < at + n) {
-          ctl->unit[0] = b0 + i;
-          ctl->unit[1] = unit - at;
-          break;
-        }
-        at += n;
-      }
-    }
+    ctl->starts[threadIdx.x] = upto - units;
     if (threadIdx.x == 0) {
-      mbar_init(&ctl->q_full, 1);
-      mbar_init(&ctl->q_conv, kTiles * kBlockM);  // every softmax thread, with or without rows
-      for (int s = 0; s < kFwdStages; ++s) {
-        mbar_init(&ctl->k_full[s], kF8 ? 2 : 1);
-        mbar_init(&ctl->v_full[s], kF8 ? 2 : 1);
-        mbar_init(&ctl->kv_empty[s], 1);
-      }
-      for (int w = 0; w < kTiles; ++w) {
-        mbar_init(&ctl->s_full[w], 1);
-        mbar_init(&ctl->p_full[w], kBlockM);
-      }
-      mbar_init(&ctl->o_full, 1);
-      for (int s = 0; s < kChunkSlots; ++s) {
-        mbar_init(&ctl->codes_full[s], 1);
-        mbar_init(&ctl->codes_empty[s], 1);
-      }
+      const int full = total / p.wave * p.wave, rest = total - full;
+      const int parts = p.part_o && rest ? chunk_parts(rest, static_cast<int>(all_steps / total), p.wave) : 1;
+      if (blockIdx.x == 0 && p.part_units) *p.part_units = parts > 1 ? rest : 0;
+      ctl->total = total;
+      ctl->full = parts > 1 ? full : total;
+      ctl->parts = parts;
       ctl->abort = 0;
-      fence_mbar_init();
     }
-    if (warp == kMmaWarp) {
-      tmem_alloc(&ctl->tmem_base, 2 * kTmemO);
-      tmem_relinquish();
-    }
-    tc_fence_before();
     __syncthreads();
-    tc_fence_after();
-    b = ctl->unit[0];
-    rq = paged_request(p.a, b);
-    const int at_unit = ctl->unit[1];
-    g = at_unit % p.a.Hkv;
-    group = chunk_units<kF8>(p, rq) - 1 - at_unit / p.a.Hkv;
   }
-  const uint32_t tmem = ctl->tmem_base;
-  const int G = p.a.G, base = rq.len - rq.n;  // position of the request's first new token
-  const int i0 = group * kTiles * p.tokens;   // the unit's first token within the request
-  const int key_hi = base + min(i0 + kTiles * p.tokens, rq.n) - 1;  // the last key any row sees
-  const int box_log2 = p.a.box_log2;
-  const int key_lo = p.a.window > 0 ? max(0, base + i0 - p.a.window + 1) >> box_log2 << box_log2 : 0;
-  // This part's 128-key tiles and 64-key steps.
-  const int halves = key_hi < key_lo ? 1 : (key_hi - key_lo) / kHalfN + 1;
-  const int tiles = (halves + 1) / 2;
-  const int tile0 = static_cast<int>(static_cast<int64_t>(tiles) * part / parts);
-  const int n_tiles = static_cast<int>(static_cast<int64_t>(tiles) * (part + 1) / parts) - tile0;
-  const int n_half = min(halves - 2 * tile0, 2 * n_tiles);
-  const int key0 = key_lo + tile0 * kBlockN;
-  // Tiles that hold tokens: the last unit of a request may have fewer than kTiles.
-  const int live = min(kTiles, (rq.n - i0 + p.tokens - 1) / p.tokens);
+  const int places = ctl->full + (ctl->total - ctl->full) * ctl->parts;
+  if (static_cast<int>(blockIdx.x) >= places) return;
 
-  if (warp >= kMmaWarp) {
-    if (warp == kMmaWarp) {
-      // ---------------------------------------------------------- MMA issuer
-      // As in the two-tile forward, the tiles in turn: S_b(h) -> P_b(h) -> O_b += P_b V(h) ->
-      // S_b(h+1) into the buffer that P_b(h) just left.
-      if (n_half > 0 && elect_one()) {
-        mbar_arrive_expect_tx(&ctl->q_full, kTiles * p.tokens * G * kHeadDim * 2);
-        for (int u = 0; u < kTiles; ++u)
-          tma_load_3d(sQ + u * kTileBytes, &tm_q, &ctl->q_full, 0, g * G, rq.t0 + i0 + u * p.tokens);
-        const uint32_t tS = tmem;
-        const uint32_t tO = tmem + kTmemO;
-        bool ok = mbar_wait(kF8 ? &ctl->q_conv : &ctl->q_full, 0, abort, &g_device_error, kDevErrTimeoutMma) &&
-                  mbar_wait(&ctl->k_full[0], 0, abort, &g_device_error, kDevErrTimeoutMma);
-        if (ok) {
-          tc_fence_after();
-#pragma unroll
-          for (int w = 0; w < kTiles; ++w) {
-            if (w >= live) break;
-            fwd_issue_qk<kF8>(tS + w * kHalfN, smem_u32(sQ + w * kTileBytes), smem_u32(sK));
-            tc_commit(&ctl->s_full[w]);
+  // A CTA takes one of every gridDim.x places in the list of units and parts,
+  // to and fro, since the units of a request get shorter along it.  (The first
+  // round's places all exist: CTAs without one have left.)
+  for (int round = 0;; ++round) {
+    const int first = round * static_cast<int>(gridDim.x);
+    if (first >= places) break;
+    const int place = first + static_cast<int>(round & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+    if (place >= places) continue;
+    int unit = place, part = 0, parts = 1, slot = 0;
+    if (place >= ctl->full) {
+      parts = ctl->parts;
+      slot = place - ctl->full;
+      unit = ctl->full + slot / parts;
+      part = slot % parts;
+    }
+    {
+      int at = ctl->starts[threadIdx.x];
+      if (unit >= at && unit < (threadIdx.x + 1 < kThreads ? ctl->starts[threadIdx.x + 1] : ctl->total)) {
+        for (int i = 0;; ++i) {
+          const int n = chunk_units<kF8>(p, paged_request(p.a, b0 + i)) * p.a.Hkv;
+          if (unit < at + n) {
+            ctl->unit[0] = b0 + i;
+            ctl->unit[1] = unit - at;
+            break;
           }
+          at += n;
         }
-        for (int h = 0; ok && h < n_half; ++h) {
-          const int j = h >> 1, s = j % kFwdStages;
-          const int hn = h + 1, jn = hn >> 1, sn = jn % kFwdStages;
-          ok = mbar_wait(&ctl->v_full[s], (j / kFwdStages) & 1, abort, &g_device_error, kDevErrTimeoutMma) &&
-               (hn >= n_half ||
-                mbar_wait(&ctl->k_full[sn], (jn / kFwdStages) & 1, abort, &g_device_error, kDevErrTimeoutMma));
-          for (int w = 0; ok && w < live; ++w) {
-            ok = mbar_wait(&ctl->p_full[w], h & 1, abort, &g_device_error, kDevErrTimeoutMma);
-            if (!ok) break;
+      }
+      if (threadIdx.x == 0) {
+        // Fresh barriers each round; everything that arrived on those of the
+        // round before has been waited for.
+        if (round > 0) {
+          for (uint64_t* bar = &ctl->q_full; bar <= &ctl->o_full; ++bar)
+            asm volatile("mbarrier.inval.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+        }
+        mbar_init(&ctl->q_full, 1);
+        mbar_init(&ctl->q_conv, kTiles * kBlockM);  // every softmax thread, with or without rows
+        for (int s = 0; s < kFwdStages; ++s) {
+          mbar_init(&ctl->k_full[s], kF8 ? 2 : 1);
+          mbar_init(&ctl->v_full[s], kF8 ? 2 : 1);
+          mbar_init(&ctl->kv_empty[s], 1);
+        }
+        for (int s = 0; s < kChunkSlots; ++s) {
+          mbar_init(&ctl->codes_full[s], 1);
+          mbar_init(&ctl->codes_empty[s], 1);
+        }
+        for (int w = 0; w < kTiles; ++w) {
+          mbar_init(&ctl->s_full[w], 1);
+          mbar_init(&ctl->p_full[w], kBlockM);
+        }
+        mbar_init(&ctl->o_full, 1);
+        fence_mbar_init();
+      }
+      if (round == 0 && warp == kMmaWarp) {
+        tmem_alloc(&ctl->tmem_base, 2 * kTmemO);
+        tmem_relinquish();
+      }
+      tc_fence_before();
+      __syncthreads();
+      tc_fence_after();
+    }
+    const uint32_t tmem = ctl->tmem_base;
+    const int b = ctl->unit[0];
+    const PagedRequest rq = paged_request(p.a, b);
+    const int g = ctl->unit[1] % p.a.Hkv;
+    const int group = chunk_units<kF8>(p, rq) - 1 - ctl->unit[1] / p.a.Hkv;
+    const int G = p.a.G, base = rq.len - rq.n;  // position of the request's first new token
+    const int i0 = group * kTiles * p.tokens;   // the unit's first token within the request
+    const int key_hi = base + min(i0 + kTiles * p.tokens, rq.n) - 1;  // the last key any row sees
+    const int box_log2 = p.a.box_log2;
+    const int key_lo = p.a.window > 0 ? max(0, base + i0 - p.a.window + 1) >> box_log2 << box_log2 : 0;
+    // This part's 128-key tiles and 64-key steps.
+    const int halves = key_hi < key_lo ? 1 : (key_hi - key_lo) / kHalfN + 1;
+    const int tiles = (halves + 1) / 2;
+    const int tile0 = static_cast<int>(static_cast<int64_t>(tiles) * part / parts);
+    const int n_tiles = static_cast<int>(static_cast<int64_t>(tiles) * (part + 1) / parts) - tile0;
+    const int n_half = min(halves - 2 * tile0, 2 * n_tiles);
+    const int key0 = key_lo + tile0 * kBlockN;
+    // Tiles that hold tokens: the last unit of a request may have fewer than kTiles.
+    const int live = min(kTiles, (rq.n - i0 + p.tokens - 1) / p.tokens);
+
+    if (warp >= kMmaWarp) {
+      if (warp == kMmaWarp) {
+        // ---------------------------------------------------------- MMA issuer
+        // As in the two-tile forward, the tiles in turn: S_b(h) -> P_b(h) -> O_b += P_b V(h) ->
+        // S_b(h+1) into the buffer that P_b(h) just left.
+        if (n_half > 0 && elect_one()) {
+          mbar_arrive_expect_tx(&ctl->q_full, kTiles * p.tokens * G * kHeadDim * 2);
+          for (int u = 0; u < kTiles; ++u)
+            tma_load_3d(sQ + u * kTileBytes, &tm_q, &ctl->q_full, 0, g * G, rq.t0 + i0 + u * p.tokens);
+          const uint32_t tS = tmem;
+          const uint32_t tO = tmem + kTmemO;
+          bool ok = mbar_wait(kF8 ? &ctl->q_conv : &ctl->q_full, 0, abort, &g_device_error, kDevErrTimeoutMma) &&
+                    mbar_wait(&ctl->k_full[0], 0, abort, &g_device_error, kDevErrTimeoutMma);
+          if (ok) {
             tc_fence_after();
-            fwd_issue_pv<kF8>(tO + w * kHeadDim, tS + w * kHalfN, smem_u32(sV + s * kTileBytes) + (h & 1) * kHalfBytes,
-                              h > 0);
-            if (hn < n_half) {
-              fwd_issue_qk<kF8>(tS + w * kHalfN, smem_u32(sQ + w * kTileBytes),
-                                smem_u32(sK + sn * kTileBytes) + (hn & 1) * kHalfBytes);
+#pragma unroll
+            for (int w = 0; w < kTiles; ++w) {
+              if (w >= live) break;
+              fwd_issue_qk<kF8>(tS + w * kHalfN, smem_u32(sQ + w * kTileBytes), smem_u32(sK));
               tc_commit(&ctl->s_full[w]);
             }
           }
-          if (ok && ((h & 1) == 1 || h == n_half - 1)) tc_commit(&ctl->kv_empty[s]);
+          for (int h = 0; ok && h < n_half; ++h) {
+            const int j = h >> 1, s = j % kFwdStages;
+            const int hn = h + 1, jn = hn >> 1, sn = jn % kFwdStages;
+            ok = mbar_wait(&ctl->v_full[s], (j / kFwdStages) & 1, abort, &g_device_error, kDevErrTimeoutMma) &&
+                 (hn >= n_half ||
+                  mbar_wait(&ctl->k_full[sn], (jn / kFwdStages) & 1, abort, &g_device_error, kDevErrTimeoutMma));
+            for (int w = 0; ok && w < live; ++w) {
+              ok = mbar_wait(&ctl->p_full[w], h & 1, abort, &g_device_error, kDevErrTimeoutMma);
+              if (!ok) break;
+              tc_fence_after();
+              fwd_issue_pv<kF8>(tO + w * kHeadDim, tS + w * kHalfN, smem_u32(sV + s * kTileBytes) + (h & 1) * kHalfBytes,
+                                h > 0);
+              if (hn < n_half) {
+                fwd_issue_qk<kF8>(tS + w * kHalfN, smem_u32(sQ + w * kTileBytes),
+                                  smem_u32(sK + sn * kTileBytes) + (hn & 1) * kHalfBytes);
+                tc_commit(&ctl->s_full[w]);
+              }
+            }
+            if (ok && ((h & 1) == 1 || h == n_half - 1)) tc_commit(&ctl->kv_empty[s]);
+          }
+          if (ok) {
+            tc_commit(&ctl->o_full);
+            // The commits that nobody else waits for, before the next round's
+            // barriers take their place.
+            for (int j = max(0, n_tiles - kFwdStages); j < n_tiles; ++j)
+              mbar_wait(&ctl->kv_empty[j % kFwdStages], (j / kFwdStages) & 1, abort, &g_device_error, kDevErrTimeoutMma);
+          }
         }
-        if (ok) tc_commit(&ctl->o_full);
-      }
-    } else if (!kF8 && warp == kCopyWarp) {
-      // ---------------------------------------------------------- TMA producer
-      // Lane x looks up the page of box x, a tile ahead of the copies.
-      const int nbox = kBlockN >> box_log2, page_mask = (1 << p.a.page_log2) - 1;
-      auto wanted = [&](int j) { return lane < nbox && key0 + j * kBlockN + (lane << box_log2) <= key_hi; };
-      auto entry = [&](int j) { return paged_entry(p.a, b, key0 + j * kBlockN + (lane << box_log2)); };
-      int next = wanted(0) ? entry(0) : 0;
-      bool ok = true;
-      for (int j = 0; ok && j < n_tiles; ++j) {
-        const int s = j % kFwdStages;
-        const int mine = wanted(j) ? paged_page(p.a, next) : p.a.num_pages;
-        if (j + 1 < n_tiles && wanted(j + 1)) next = entry(j + 1);
-        if (j >= kFwdStages)
-          ok = warp_all(mbar_wait(&ctl->kv_empty[s], ((j / kFwdStages) - 1) & 1, abort, &g_device_error,
-                                  kDevErrTimeoutProducer));
-        if (!ok) break;
-        if (elect_one()) {
-          mbar_arrive_expect_tx(&ctl->k_full[s], kTileBytes);
-          mbar_arrive_expect_tx(&ctl->v_full[s], kTileBytes);
-        }
-        __syncwarp();
-        for (int y = 0; y < 2 * nbox; ++y) {  // K first: S waits for it
-          const bool is_v = y >= nbox;
-          const int x = is_v ? y - nbox : y;
-          const int page = __shfl_sync(0xffffffffu, mine, x);
-          const int at = (key0 + j * kBlockN + (x << box_log2)) & page_mask;
-          if (elect_one())
-            tma_load_4d((is_v ? sV : sK) + s * kTileBytes + (x << box_log2) * kHeadDim * 2, is_v ? &tm_v : &tm_k,
-                        is_v ? &ctl->v_full[s] : &ctl->k_full[s], 0, at, g, page);
-          __syncwarp();
-        }
-      }
-    } else if (kF8 && warp == kCopyWarp) {
-      // ------------------------------------------------------ e4m3: TMA producer
-      // Slot q holds 64 keys: of tile q / 4 those of K, two slots, then those of V.
-      const int nbox = kBlockN >> box_log2, page_mask = (1 << p.a.page_log2) - 1;
-      const int per_slot = kChunkSlotKeys >> box_log2;
-      auto wanted = [&](int j) { return lane < nbox && key0 + j * kBlockN + (lane << box_log2) <= key_hi; };
-      auto entry = [&](int j) { return paged_entry(p.a, b, key0 + j * kBlockN + (lane << box_log2)); };
-      int next = wanted(0) ? entry(0) : 0, mine = 0;
-      bool ok = true;
-      for (int q = 0; ok && q < 4 * n_tiles; ++q) {
-        const int j = q >> 2, e = q & 3, at_slot = q % kChunkSlots;
-        if (e == 0) {
-          mine = wanted(j) ? paged_page(p.a, next) : p.a.num_pages;
+      } else if (!kF8 && warp == kCopyWarp) {
+        // ---------------------------------------------------------- TMA producer
+        // Lane x looks up the page of box x, a tile ahead of the copies.
+        const int nbox = kBlockN >> box_log2, page_mask = (1 << p.a.page_log2) - 1;
+        auto wanted = [&](int j) { return lane < nbox && key0 + j * kBlockN + (lane << box_log2) <= key_hi; };
+        auto entry = [&](int j) { return paged_entry(p.a, b, key0 + j * kBlockN + (lane << box_log2)); };
+        int next = wanted(0) ? entry(0) : 0;
+        bool ok = true;
+        for (int j = 0; ok && j < n_tiles; ++j) {
+          const int s = j % kFwdStages;
+          const int mine = wanted(j) ? paged_page(p.a, next) : p.a.num_pages;
           if (j + 1 < n_tiles && wanted(j + 1)) next = entry(j + 1);
-        }
-        if (q >= kChunkSlots)
-          ok = warp_all(mbar_wait(&ctl->codes_empty[at_slot], ((q / kChunkSlots) - 1) & 1, abort, &g_device_error,
-                                  kDevErrTimeoutProducer));
-        if (!ok) break;
-        uint64_t* full = &ctl->codes_full[at_slot];
-        uint8_t* to = sB + at_slot * kChunkSlotBytes;
-        if (elect_one()) mbar_arrive_expect_tx(full, kChunkSlotBytes);
-        __syncwarp();
-        for (int x = 0; x < per_slot; ++x) {
-          const int box = (e & 1) * per_slot + x;
-          const int page = __shfl_sync(0xffffffffu, mine, box);
-          const int at = (key0 + j * kBlockN + (box << box_log2)) & page_mask;
-          if (elect_one())
-            tma_load_4d(to + (x << box_log2) * kHeadDim, e < 2 ? &tm_k : &tm_v, full, 0, at, g, page);
-          __syncwarp();
-        }
-      }
-    } else if (kF8) {
-      // ------------------------------------------------------------ e4m3: widen
-      // This warp takes every other slot.  Rows that no row of the request sees
-      // become zeros.
-      bool ok = true;
-      for (int q = warp - kCopyWarp - 1; q < 4 * n_tiles; q += 2) {
-        const int j = q >> 2, e = q & 3, s = j % kFwdStages, at_slot = q % kChunkSlots;
-        if (e < 2 && j >= kFwdStages)
-          ok = warp_all(mbar_wait(&ctl->kv_empty[s], ((j / kFwdStages) - 1) & 1, abort, &g_device_error,
-                                  kDevErrTimeoutProducer));
-        ok = ok && warp_all(mbar_wait(&ctl->codes_full[at_slot], (q / kChunkSlots) & 1, abort, &g_device_error,
-                                      kDevErrTimeoutProducer));
-        if (!ok) break;
-        uint4 v[8];
-#pragma unroll
-        for (int u = 0; u < 8; ++u) {  // 16 codes: row lane / 4 + 8 u, 16-byte piece lane % 4
-          const int row = (lane >> 2) + 8 * u;
-          v[u] = *reinterpret_cast<const uint4*>(sB + at_slot * kChunkSlotBytes + row * kHeadDim +
-                                                 (((lane & 3) ^ ((row >> 1) & 3)) << 4));
-        }
-        uint8_t* tile = (e < 2 ? sK : sV) + s * kTileBytes + (e & 1) * kChunkSlotKeys * 128;
-        const int key = key0 + j * kBlockN + (e & 1) * kChunkSlotKeys + (lane >> 2);
-#pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          const int row = (lane >> 2) + 8 * u;
-          if (key + 8 * u < rq.lo || key + 8 * u >= rq.len) v[u] = make_uint4(0u, 0u, 0u, 0u);
-          const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
-#pragma unroll
-          for (int c = 0; c < 2; ++c)
-            *reinterpret_cast<uint4*>(tile + row * 128 + (((2 * (lane & 3) + c) ^ (row & 7)) << 4)) =
-                make_uint4(e4m3x2_to_f16x2(w[2 * c]), e4m3x2_to_f16x2(w[2 * c] >> 16), e4m3x2_to_f16x2(w[2 * c + 1]),
-                           e4m3x2_to_f16x2(w[2 * c + 1] >> 16));
-        }
-        fence_proxy_async_smem();  // the tile for the MMA; the slot's reads before its next copy
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&ctl->codes_empty[at_slot]);
-          mbar_arrive(e < 2 ? &ctl->k_full[s] : &ctl->v_full[s]);
-        }
-      }
-    }
-  } else {
-    // --------------------------------------------- softmax (1 row per thread)
-    const int wg = warp >> 2;
-    const int r = threadIdx.x & (kBlockM - 1);
-    const int row_t = r / G;
-    const int it = i0 + wg * p.tokens + row_t;  // token within the request
-    const bool valid = row_t < p.tokens && it < rq.n;
-    const int h = g * G + r - row_t * G;
-    // Allowed keys [lo_r, hi_r] of this row; empty for idle rows.
-    const int hi_r = valid ? base + it : -1;
-    const int lo_r = valid && p.a.window > 0 ? max(0, hi_r - p.a.window + 1) : 0;
-    // Keys that every row of this warpgroup's tile sees: [all_lo, all_hi].
-    const int w0 = i0 + wg * p.tokens, w1 = min(w0 + p.tokens, rq.n) - 1;
-    const int all_hi = w0 <= w1 ? base + w0 : -1;
-    const int all_lo = p.a.window > 0 ? max(0, base + w1 - p.a.window + 1) : 0;
-    float m_ref = -INFINITY, l = 0.f;
-    const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t tS = tmem + lane_base + wg * kHalfN;
-    const uint32_t tO = tmem + lane_base + kTmemO + wg * kHeadDim;
-    const float sl2 = kF8 ? p.a.scale_log2 * __ldg(p.a.k_scale + g) : p.a.scale_log2;
-    // A part of a unit with fewer key tiles than parts may have none.
-    bool ok = n_half > 0 && wg < live;
-    const float s2 = valid ? __ldg(p.a.sinks + h) * kLog2e : 0.f;
-    if constexpr (kF8) {
-      if (n_half > 0 && wg >= live) mbar_arrive(&ctl->q_conv);
-      ok = ok && warp_all(mbar_wait(&ctl->q_full, 0, abort, &g_device_error, kDevErrTimeoutSoftmax));
-      if (ok) {
-        // Rows of 128 bytes, so elementwise in place whatever the swizzle.
-        uint32_t* row = reinterpret_cast<uint32_t*>(sQ + wg * kTileBytes + r * 128);
-#pragma unroll 8
-        for (int c = 0; c < 32; ++c) {
-          const int at = (c + r) & 31;  // 32 lanes, 32 banks
-          row[at] = bf16x2_to_f16x2_sat(row[at]);
-        }
-        fence_proxy_async_smem();
-        mbar_arrive(&ctl->q_conv);
-      }
-    }
-
-    for (int hs = 0; ok && hs < n_half; ++hs) {
-      ok = warp_all(mbar_wait(&ctl->s_full[wg], hs & 1, abort, &g_device_error, kDevErrTimeoutSoftmax));
-      if (!ok) break;
-      tc_fence_after();
-      uint32_t sr[kHalfN];
-      tmem_ld64(tS, sr);
-      const int ks = key0 + hs * kHalfN;
-      if (ks + kHalfN - 1 > all_hi || ks < all_lo) {
-        // One bit per key: a test and a selection each, where two compares of
-        // the key's place made a window layer's steps half as long again.
-        const uint32_t seen[2] = {chunk_bits(lo_r - ks, hi_r - ks), chunk_bits(lo_r - ks - 32, hi_r - ks - 32)};
-#pragma unroll
-        for (int c = 0; c < kHalfN; ++c) sr[c] = seen[c >> 5] >> (c & 31) & 1u ? sr[c] : 0xFF800000u;
-      }
-      const FwdRowStep st = fwd_row_step<false, kF8>(sr, 0, 0, sl2, m_ref);
-      l = l * st.alpha + st.sum;
-      __syncwarp();
-      tmem_st32(tS, sr);
-      if (hs > 0 && __any_sync(0xffffffffu, st.need)) {
-        uint32_t o[kHeadDim];
-        tmem_ld64(tO, o);
-#pragma unroll
-        for (int c = 0; c < kHeadDim; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * st.alpha);
-        tmem_st32(tO, o);
-        tmem_st32(tO + 32, o + 32);
-      }
-      m_ref = st.m_new;
-      if constexpr (!kF8) {
-        // Keys of the step that no row of the request sees: zero rows of V.
-        // Both warpgroups write them, each before its own PV.
-        if (ks < rq.lo || ks + kHalfN > rq.len) {
-          const int j = hs >> 1, s = j % kFwdStages;
-          ok = warp_all(mbar_wait(&ctl->v_full[s], (j / kFwdStages) & 1, abort, &g_device_error, kDevErrTimeoutSoftmax));
+          if (j >= kFwdStages)
+            ok = warp_all(mbar_wait(&ctl->kv_empty[s], ((j / kFwdStages) - 1) & 1, abort, &g_device_error,
+                                    kDevErrTimeoutProducer));
           if (!ok) break;
-          const int key = ks + (r >> 1);
-          if (key < rq.lo || key >= rq.len) {
-            uint4* row = reinterpret_cast<uint4*>(sV + s * kTileBytes + ((hs & 1) * kHalfN + (r >> 1)) * 128 + (r & 1) * 64);
+          if (elect_one()) {
+            mbar_arrive_expect_tx(&ctl->k_full[s], kTileBytes);
+            mbar_arrive_expect_tx(&ctl->v_full[s], kTileBytes);
+          }
+          __syncwarp();
+          for (int y = 0; y < 2 * nbox; ++y) {  // K first: S waits for it
+            const bool is_v = y >= nbox;
+            const int x = is_v ? y - nbox : y;
+            const int page = __shfl_sync(0xffffffffu, mine, x);
+            const int at = (key0 + j * kBlockN + (x << box_log2)) & page_mask;
+            if (elect_one())
+              tma_load_4d((is_v ? sV : sK) + s * kTileBytes + (x << box_log2) * kHeadDim * 2, is_v ? &tm_v : &tm_k,
+                          is_v ? &ctl->v_full[s] : &ctl->k_full[s], 0, at, g, page);
+            __syncwarp();
+          }
+        }
+      } else if (kF8 && warp == kCopyWarp) {
+        // ------------------------------------------------------ e4m3: TMA producer
+        // Slot q holds 64 keys: of tile q / 4 those of K, two slots, then those of V.
+        const int nbox = kBlockN >> box_log2, page_mask = (1 << p.a.page_log2) - 1;
+        const int per_slot = kChunkSlotKeys >> box_log2;
+        auto wanted = [&](int j) { return lane < nbox && key0 + j * kBlockN + (lane << box_log2) <= key_hi; };
+        auto entry = [&](int j) { return paged_entry(p.a, b, key0 + j * kBlockN + (lane << box_log2)); };
+        int next = wanted(0) ? entry(0) : 0, mine = 0;
+        bool ok = true;
+        for (int q = 0; ok && q < 4 * n_tiles; ++q) {
+          const int j = q >> 2, e = q & 3, at_slot = q % kChunkSlots;
+          if (e == 0) {
+            mine = wanted(j) ? paged_page(p.a, next) : p.a.num_pages;
+            if (j + 1 < n_tiles && wanted(j + 1)) next = entry(j + 1);
+          }
+          if (q >= kChunkSlots)
+            ok = warp_all(mbar_wait(&ctl->codes_empty[at_slot], ((q / kChunkSlots) - 1) & 1, abort, &g_device_error,
+                                    kDevErrTimeoutProducer));
+          if (!ok) break;
+          uint64_t* full = &ctl->codes_full[at_slot];
+          uint8_t* to = sB + at_slot * kChunkSlotBytes;
+          if (elect_one()) mbar_arrive_expect_tx(full, kChunkSlotBytes);
+          __syncwarp();
+          for (int x = 0; x < per_slot; ++x) {
+            const int box = (e & 1) * per_slot + x;
+            const int page = __shfl_sync(0xffffffffu, mine, box);
+            const int at = (key0 + j * kBlockN + (box << box_log2)) & page_mask;
+            if (elect_one())
+              tma_load_4d(to + (x << box_log2) * kHeadDim, e < 2 ? &tm_k : &tm_v, full, 0, at, g, page);
+            __syncwarp();
+          }
+        }
+      } else if (kF8) {
+        // ------------------------------------------------------------ e4m3: widen
+        // This warp takes every other slot.  Rows that no row of the request sees
+        // become zeros.
+        bool ok = true;
+        for (int q = warp - kCopyWarp - 1; q < 4 * n_tiles; q += 2) {
+          const int j = q >> 2, e = q & 3, s = j % kFwdStages, at_slot = q % kChunkSlots;
+          if (e < 2 && j >= kFwdStages)
+            ok = warp_all(mbar_wait(&ctl->kv_empty[s], ((j / kFwdStages) - 1) & 1, abort, &g_device_error,
+                                    kDevErrTimeoutProducer));
+          ok = ok && warp_all(mbar_wait(&ctl->codes_full[at_slot], (q / kChunkSlots) & 1, abort, &g_device_error,
+                                        kDevErrTimeoutProducer));
+          if (!ok) break;
+          uint4 v[8];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) row[c] = make_uint4(0u, 0u, 0u, 0u);
+          for (int u = 0; u < 8; ++u) {  // 16 codes: row lane / 4 + 8 u, 16-byte piece lane % 4
+            const int row = (lane >> 2) + 8 * u;
+            v[u] = *reinterpret_cast<const uint4*>(sB + at_slot * kChunkSlotBytes + row * kHeadDim +
+                                                   (((lane & 3) ^ ((row >> 1) & 3)) << 4));
+          }
+          uint8_t* tile = (e < 2 ? sK : sV) + s * kTileBytes + (e & 1) * kChunkSlotKeys * 128;
+          const int key = key0 + j * kBlockN + (e & 1) * kChunkSlotKeys + (lane >> 2);
+#pragma unroll
+          for (int u = 0; u < 8; ++u) {
+            const int row = (lane >> 2) + 8 * u;
+            if (key + 8 * u < rq.lo || key + 8 * u >= rq.len) v[u] = make_uint4(0u, 0u, 0u, 0u);
+            const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+              *reinterpret_cast<uint4*>(tile + row * 128 + (((2 * (lane & 3) + c) ^ (row & 7)) << 4)) =
+                  make_uint4(e4m3x2_to_f16x2(w[2 * c]), e4m3x2_to_f16x2(w[2 * c] >> 16), e4m3x2_to_f16x2(w[2 * c + 1]),
+                             e4m3x2_to_f16x2(w[2 * c + 1] >> 16));
+          }
+          fence_proxy_async_smem();  // the tile for the MMA; the slot's reads before its next copy
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&ctl->codes_empty[at_slot]);
+            mbar_arrive(e < 2 ? &ctl->k_full[s] : &ctl->v_full[s]);
+          }
+        }
+      }
+    } else {
+      // --------------------------------------------- softmax (1 row per thread)
+      const int wg = warp >> 2;
+      const int r = threadIdx.x & (kBlockM - 1);
+      const int row_t = r / G;
+      const int it = i0 + wg * p.tokens + row_t;  // token within the request
+      const bool valid = row_t < p.tokens && it < rq.n;
+      const int h = g * G + r - row_t * G;
+      // Allowed keys [lo_r, hi_r] of this row; empty for idle rows.
+      const int hi_r = valid ? base + it : -1;
+      const int lo_r = valid && p.a.window > 0 ? max(0, hi_r - p.a.window + 1) : 0;
+      // Keys that every row of this warpgroup's tile sees: [all_lo, all_hi].
+      const int w0 = i0 + wg * p.tokens, w1 = min(w0 + p.tokens, rq.n) - 1;
+      const int all_hi = w0 <= w1 ? base + w0 : -1;
+      const int all_lo = p.a.window > 0 ? max(0, base + w1 - p.a.window + 1) : 0;
+      float m_ref = -INFINITY, l = 0.f;
+      const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+      const uint32_t tS = tmem + lane_base + wg * kHalfN;
+      const uint32_t tO = tmem + lane_base + kTmemO + wg * kHeadDim;
+      const float sl2 = kF8 ? p.a.scale_log2 * __ldg(p.a.k_scale + g) : p.a.scale_log2;
+      // A part of a unit with fewer key tiles than parts may have none.
+      bool ok = n_half > 0 && wg < live;
+      const float s2 = valid ? __ldg(p.a.sinks + h) * kLog2e : 0.f;
+      if constexpr (kF8) {
+        if (n_half > 0 && wg >= live) mbar_arrive(&ctl->q_conv);
+        ok = ok && warp_all(mbar_wait(&ctl->q_full, 0, abort, &g_device_error, kDevErrTimeoutSoftmax));
+        if (ok) {
+          // Rows of 128 bytes, so elementwise in place whatever the swizzle.
+          uint32_t* row = reinterpret_cast<uint32_t*>(sQ + wg * kTileBytes + r * 128);
+#pragma unroll 8
+          for (int c = 0; c < 32; ++c) {
+            const int at = (c + r) & 31;  // 32 lanes, 32 banks
+            row[at] = bf16x2_to_f16x2_sat(row[at]);
           }
           fence_proxy_async_smem();
+          mbar_arrive(&ctl->q_conv);
         }
       }
-      tc_fence_before();
-      mbar_arrive(&ctl->p_full[wg]);
-    }
 
-    // ---------------------------------------------------------------- epilogue
-    if (n_half == 0) {
-      p.part_ml[static_cast<long long>(slot) * kTiles * kBlockM + wg * kBlockM + r] = make_float2(-INFINITY, 0.f);
-      if (part == 0 && threadIdx.x == 0) p.part_unit[slot / parts] = make_int4(b, group, g, parts);
-    }
-    if (ok) ok = mbar_wait(&ctl->o_full, 0, abort, &g_device_error, kDevErrTimeoutEpilogue);
-    ok = warp_all(ok);
-    if (ok) {
-      tc_fence_after();
-      uint32_t o[kHeadDim];
-      __syncwarp();
-      tmem_ld64(tO, o);
-      const float vs = kF8 ? __ldg(p.a.v_scale + g) : 1.f;
-      if (parts > 1) {
-        const long long at = static_cast<long long>(slot) * kTiles * kBlockM + wg * kBlockM + r;
-        p.part_ml[at] = make_float2(m_ref, l);
+      for (int hs = 0; ok && hs < n_half; ++hs) {
+        ok = warp_all(mbar_wait(&ctl->s_full[wg], hs & 1, abort, &g_device_error, kDevErrTimeoutSoftmax));
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t sr[kHalfN];
+        tmem_ld64(tS, sr);
+        const int ks = key0 + hs * kHalfN;
+        if (ks + kHalfN - 1 > all_hi || ks < all_lo) {
+          // One bit per key: a test and a selection each, where two compares of
+          // the key's place made a window layer's steps half as long again.
+          const uint32_t seen[2] = {chunk_bits(lo_r - ks, hi_r - ks), chunk_bits(lo_r - ks - 32, hi_r - ks - 32)};
+#pragma unroll
+          for (int c = 0; c < kHalfN; ++c) sr[c] = seen[c >> 5] >> (c & 31) & 1u ? sr[c] : 0xFF800000u;
+        }
+        const FwdRowStep st = fwd_row_step<false, kF8>(sr, 0, 0, sl2, m_ref);
+        l = l * st.alpha + st.sum;
+        __syncwarp();
+        tmem_st32(tS, sr);
+        if (hs > 0 && __any_sync(0xffffffffu, st.need)) {
+          uint32_t o[kHeadDim];
+          tmem_ld64(tO, o);
+#pragma unroll
+          for (int c = 0; c < kHeadDim; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * st.alpha);
+          tmem_st32(tO, o);
+          tmem_st32(tO + 32, o + 32);
+        }
+        m_ref = st.m_new;
+        if constexpr (!kF8) {
+          // Keys of the step that no row of the request sees: zero rows of V.
+          // Both warpgroups write them, each before its own PV.
+          if (ks < rq.lo || ks + kHalfN > rq.len) {
+            const int j = hs >> 1, s = j % kFwdStages;
+            ok = warp_all(mbar_wait(&ctl->v_full[s], (j / kFwdStages) & 1, abort, &g_device_error, kDevErrTimeoutSoftmax));
+            if (!ok) break;
+            const int key = ks + (r >> 1);
+            if (key < rq.lo || key >= rq.len) {
+              uint4* row = reinterpret_cast<uint4*>(sV + s * kTileBytes + ((hs & 1) * kHalfN + (r >> 1)) * 128 + (r & 1) * 64);
+#pragma unroll
+              for (int c = 0; c < 4; ++c) row[c] = make_uint4(0u, 0u, 0u, 0u);
+            }
+            fence_proxy_async_smem();
+          }
+        }
+        tc_fence_before();
+        mbar_arrive(&ctl->p_full[wg]);
+      }
+
+      // ---------------------------------------------------------------- epilogue
+      if (n_half == 0) {
+        p.part_ml[static_cast<long long>(slot) * kTiles * kBlockM + wg * kBlockM + r] = make_float2(-INFINITY, 0.f);
         if (part == 0 && threadIdx.x == 0) p.part_unit[slot / parts] = make_int4(b, group, g, parts);
-        float4* dst = reinterpret_cast<float4*>(p.part_o + at * kHeadDim);
-        if (valid) {
+      }
+      if (ok) ok = mbar_wait(&ctl->o_full, 0, abort, &g_device_error, kDevErrTimeoutEpilogue);
+      ok = warp_all(ok);
+      if (ok) {
+        tc_fence_after();
+        uint32_t o[kHeadDim];
+        __syncwarp();
+        tmem_ld64(tO, o);
+        const float vs = kF8 ? __ldg(p.a.v_scale + g) : 1.f;
+        if (parts > 1) {
+          const long long at = static_cast<long long>(slot) * kTiles * kBlockM + wg * kBlockM + r;
+          p.part_ml[at] = make_float2(m_ref, l);
+          if (part == 0 && threadIdx.x == 0) p.part_unit[slot / parts] = make_int4(b, group, g, parts);
+          float4* dst = reinterpret_cast<float4*>(p.part_o + at * kHeadDim);
+          if (valid) {
 #pragma unroll
-          for (int c = 0; c < kHeadDim / 4; ++c)
-            dst[c] = make_float4(__uint_as_float(o[4 * c]) * vs, __uint_as_float(o[4 * c + 1]) * vs,
-                                 __uint_as_float(o[4 * c + 2]) * vs, __uint_as_float(o[4 * c + 3]) * vs);
-        }
-      } else if (valid) {
-        const float top = fmaxf(s2, m_ref);
-        float f = 0.f, all = 0.f;
-        if (top != -INFINITY) {
-          f = ex2_approx(m_ref - top);
-          all = fmaf(l, f, s2 == top ? 1.f : ex2_approx(s2 - top));
-        }
-        f = all > 0.f ? vs * f / all : 0.f;
-        const int t = rq.t0 + it;
-        uint4* dst = reinterpret_cast<uint4*>(p.a.out + (static_cast<long long>(t) * p.a.Hq + h) * kHeadDim);
+            for (int c = 0; c < kHeadDim / 4; ++c)
+              dst[c] = make_float4(__uint_as_float(o[4 * c]) * vs, __uint_as_float(o[4 * c + 1]) * vs,
+                                   __uint_as_float(o[4 * c + 2]) * vs, __uint_as_float(o[4 * c + 3]) * vs);
+          }
+        } else if (valid) {
+          const float top = fmaxf(s2, m_ref);
+          float f = 0.f, all = 0.f;
+          if (top != -INFINITY) {
+            f = ex2_approx(m_ref - top);
+            all = fmaf(l, f, s2 == top ? 1.f : ex2_approx(s2 - top));
+          }
+          f = all > 0.f ? vs * f / all : 0.f;
+          const int t = rq.t0 + it;
+          uint4* dst = reinterpret_cast<uint4*>(p.a.out + (static_cast<long long>(t) * p.a.Hq + h) * kHeadDim);
 #pragma unroll
-        for (int c = 0; c < kHeadDim / 8; ++c) {
-          uint4 v;
-          v.x = pack_bf16x2(__uint_as_float(o[8 * c + 0]) * f, __uint_as_float(o[8 * c + 1]) * f);
-          v.y = pack_bf16x2(__uint_as_float(o[8 * c + 2]) * f, __uint_as_float(o[8 * c + 3]) * f);
-          v.z = pack_bf16x2(__uint_as_float(o[8 * c + 4]) * f, __uint_as_float(o[8 * c + 5]) * f);
-          v.w = pack_bf16x2(__uint_as_float(o[8 * c + 6]) * f, __uint_as_float(o[8 * c + 7]) * f);
-          dst[c] = v;
+          for (int c = 0; c < kHeadDim / 8; ++c) {
+            uint4 v;
+            v.x = pack_bf16x2(__uint_as_float(o[8 * c + 0]) * f, __uint_as_float(o[8 * c + 1]) * f);
+            v.y = pack_bf16x2(__uint_as_float(o[8 * c + 2]) * f, __uint_as_float(o[8 * c + 3]) * f);
+            v.z = pack_bf16x2(__uint_as_float(o[8 * c + 4]) * f, __uint_as_float(o[8 * c + 5]) * f);
+            v.w = pack_bf16x2(__uint_as_float(o[8 * c + 6]) * f, __uint_as_float(o[8 * c + 7]) * f);
+            dst[c] = v;
+          }
+          p.a.lse[static_cast<long long>(h) * p.a.T + t] = all > 0.f ? (top + __log2f(all)) * kLn2 : -INFINITY;
         }
-        p.a.lse[static_cast<long long>(h) * p.a.T + t] = all > 0.f ? (top + __log2f(all)) * kLn2 : -INFINITY;
       }
     }
+
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (ctl->abort) break;
   }
 
-  tc_fence_before();
   __syncthreads();
-  if (warp == kMmaWarp) {
-    tc_fence_after();
-    tmem_dealloc(tmem, 2 * kTmemO);
-  }
+  if (warp == kMmaWarp) tmem_dealloc(ctl->tmem_base, 2 * kTmemO);
 }
 
 // Joins the parts of the cut units and adds the sink.  One CTA per cut unit
 // and 32 of its rows; half a warp per row, four dims per lane.
 template <bool kF8>
 __global__ void __launch_bounds__(256) sink_attn_paged_chunk_join_kernel(const __grid_constant__ ChunkParams p) {
+  pdl_launch_dependents();
   pdl_wait();
   const int i = blockIdx.x;
   if (i >= __ldcg(p.part_units)) return;

@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
   int* pre = reinterpret_cast<int*>(ctl + 1);
   volatile int* abort = &ctl->abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  pdl_launch_dependents();  // the combine kernel waits for this one's end by itself
+  pdl_launch_dependents();  // the joins wait for this kernel's end by themselves
 
   const int per_group = p.per_chunk * p.row_parts;  // warps of a worker
   const int groups = kWarps / per_group;             // workers of this CTA
@@ -330,6 +330,10 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
       ++j;
       if (++s == stages) s = 0, ++turn;
     }
+    // Beside the chunk kernel: this one has not ended before that has, so that
+    // whoever waits for this one (the joins, the next call) waits for both.  One
+    // CTA sees to it; the others make room.
+    if (blockIdx.x == 0) pdl_wait();
     return;
   }
 

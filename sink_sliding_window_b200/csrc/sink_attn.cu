@@ -777,24 +777,29 @@ bool rows_never_cut(const PagedParams& p) {
   return (keys + lead + kRowsKeys<kF8> - 1) / kRowsKeys<kF8> <= 2 * kRowsSnap<kF8> + 1;
 }
 
-// Launches a 256-thread kernel that waits by itself for the kernel before it.
-template <typename P>
-bool launch_join(void (*kernel)(P), dim3 grid, const P& p, cudaStream_t st) {
+// Launches a kernel that may start before the one before it on the stream has
+// ended, and waits for that (griddepcontrol.wait) where it needs to.
+template <typename... A>
+bool launch_early(void (*kernel)(A...), dim3 grid, unsigned threads, size_t smem, cudaStream_t st, const A&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
-  cfg.blockDim = dim3(256, 1, 1);
+  cfg.blockDim = dim3(threads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess;
+  return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess;
 }
 
+// `beside`: the chunk kernel runs before it on the stream.  The two share
+// nothing but the SMs, which take the pieces of this kernel as they run out of
+// chunks, so it does not wait for the other to end.
 template <bool kF8, int kR>
-bool launch_rows(PagedParams& p, const sink_attn_paged_dims* d, const void* k_cache, const void* v_cache,
-                 cudaStream_t st) {
+bool launch_rows(PagedParams& p, const sink_attn_paged_dims* d, const void* k_cache, const void* v_cache, bool beside,
+                 dim3* join, cudaStream_t st) {
   const int box = std::min(d->page_size, kRowsKeys<kF8>);
   p.box_log2 = ilog2_exact(box);
   CUtensorMap tm_k, tm_v;
@@ -802,24 +807,27 @@ bool launch_rows(PagedParams& p, const sink_attn_paged_dims* d, const void* k_ca
       !make_map_paged(&tm_v, v_cache, d, kF8, box, p.per_chunk)) return false;
   static SmemAttrOnce smem_set;
   if (!smem_set.ensure(sink_attn_paged_rows_kernel<kF8, kR>, rows_smem_bytes(kPagedMaxBatch))) return false;
-  const bool join = !rows_never_cut<kF8>(p);
-  if (!join) p.part_unit = nullptr;
+  const bool cut = !rows_never_cut<kF8>(p);
+  if (!cut) p.part_unit = nullptr;
   // No more CTAs than the most blocks there can be give work to.
   const int64_t keys = p.window > 0 ? static_cast<int64_t>(p.window) + p.few - 1 + box : INT64_MAX;
   const int64_t most = (std::min(keys, int64_t(p.max_pages) << p.page_log2) + kRowsKeys<kF8> - 1) / kRowsKeys<kF8> + 1;
   const int64_t workers = (most * p.batch * p.chunks + kRowsMinBlocks - 1) / kRowsMinBlocks;
   const int per_group = p.per_chunk * p.row_parts, groups = kRowsWarps / per_group;
   const int ctas = static_cast<int>(std::min<int64_t>(kPagedCtas, workers));
+  if (cut) *join = dim3(ctas * groups, per_group);
+  if (beside)
+    return launch_early(sink_attn_paged_rows_kernel<kF8, kR>, dim3(ctas), kRowsThreads, rows_smem_bytes(p.batch), st, tm_k,
+                        tm_v, p);
   sink_attn_paged_rows_kernel<kF8, kR><<<ctas, kRowsThreads, rows_smem_bytes(p.batch), st>>>(tm_k, tm_v, p);
-  if (cudaPeekAtLastError() != cudaSuccess) return false;
-  if (!join) return true;
-  return launch_join(sink_attn_paged_join_kernel<kR>, dim3(ctas * groups, per_group), p, st);
+  return cudaPeekAtLastError() == cudaSuccess;
 }
 
 template <bool kF8>
 bool launch_rows(int kR, PagedParams& p, const sink_attn_paged_dims* d, const void* k_cache, const void* v_cache,
-                 cudaStream_t st) {
-  return kR == 8 ? launch_rows<kF8, 8>(p, d, k_cache, v_cache, st) : launch_rows<kF8, 16>(p, d, k_cache, v_cache, st);
+                 bool beside, dim3* join, cudaStream_t st) {
+  return kR == 8 ? launch_rows<kF8, 8>(p, d, k_cache, v_cache, beside, join, st)
+                 : launch_rows<kF8, 16>(p, d, k_cache, v_cache, beside, join, st);
 }
 
 // The query tile of the chunk kernel, `tokens` tokens of one group of heads.
@@ -838,9 +846,9 @@ bool make_map_paged_q(CUtensorMap* map, const sink_attn_paged_dims* d, const voi
 
 template <bool kF8>
 bool launch_chunks(ChunkParams& p, const sink_attn_paged_dims* d, const void* k_cache, const void* v_cache,
-                   const PagedSplit& split, cudaStream_t st) {
+                   const PagedSplit& split, dim3* join, cudaStream_t st) {
   const ChunkBound bound = chunk_bound<kF8>(d, split, p.a.window);
-  if (bound.units + bound.parts > 0x7fffffff) return false;
+  if (bound.units > (1 << 30)) return false;
   p.wave = kChunkPerSm<kF8> * kChunkSms;
   CUtensorMap tm_q, tm_k, tm_v;
   const int box = std::min(d->page_size, kHalfN);
@@ -851,12 +859,20 @@ bool launch_chunks(ChunkParams& p, const sink_attn_paged_dims* d, const void* k_
   static SmemAttrOnce smem_set;
   if (!smem_set.ensure(sink_attn_paged_chunk_kernel<kF8>, chunk_smem_bytes<kF8>())) return false;
   if (bound.parts == 0) p.part_o = nullptr;
-  sink_attn_paged_chunk_kernel<kF8><<<static_cast<unsigned>(bound.units + bound.parts), kChunkThreads<kF8>,
-                                      chunk_smem_bytes<kF8>(), st>>>(tm_q, tm_k, tm_v, p);
-  if (cudaPeekAtLastError() != cudaSuccess) return false;
-  if (bound.parts == 0) return true;
-  const unsigned cut = static_cast<unsigned>(std::min<int64_t>(bound.units, p.wave - 1));
-  return launch_join(sink_attn_paged_chunk_join_kernel<kF8>, dim3(cut, kChunkTiles<kF8> * kBlockM / 32), p, st);
+  // Units too short to be cut (a window): one wave of CTAs, each taking its
+  // turns, which saves every unit the start of a CTA.  Longer ones: a CTA for
+  // each as far as four waves go, which the SMs even out among themselves;
+  // but one wave again when most requests must be single tokens, since the
+  // few-rows kernel can take its place beside this one only when all CTAs of
+  // this one have started.  (Window-128 chunks: 86 us in turns, 92 with a CTA
+  // each; 2048 tokens of 32768: 1493 in turns, 1410; 5 chunks and 28 tokens:
+  // 77 in turns, 87.)
+  const bool turns = bound.parts == 0 || d->total_tokens < static_cast<int64_t>(d->batch) * d->max_new / 2;
+  const int64_t places = bound.units + bound.parts;
+  const unsigned ctas = static_cast<unsigned>(std::min<int64_t>(places, (turns ? 1 : kChunkMaxWaves + 1) * p.wave));
+  sink_attn_paged_chunk_kernel<kF8><<<ctas, kChunkThreads<kF8>, chunk_smem_bytes<kF8>(), st>>>(tm_q, tm_k, tm_v, p);
+  if (bound.parts) *join = dim3(static_cast<unsigned>(std::min<int64_t>(bound.units, p.wave - 1)), kChunkTiles<kF8> * kBlockM / 32);
+  return cudaPeekAtLastError() == cudaSuccess;
 }
 
 sink_attn_status paged_attn_impl(const sink_attn_paged_dims* d, const void* q, const void* k_cache,
@@ -911,20 +927,27 @@ sink_attn_status paged_attn_impl(const sink_attn_paged_dims* d, const void* q, c
   p.part_ml = reinterpret_cast<float2*>(base + ws.ml);
   p.part_o = reinterpret_cast<float*>(base + ws.o);
   cudaStream_t st_ = static_cast<cudaStream_t>(stream);
+  ChunkParams c;
+  dim3 chunk_join(0), rows_join(0);
   if (split.chunks) {
-    ChunkParams c;
     c.a = p;
     c.tokens = kBlockM / p.G;
     c.part_units = reinterpret_cast<int*>(base + ws.chunk_units);
     c.part_unit = reinterpret_cast<int4*>(base + ws.chunk_unit);
     c.part_ml = reinterpret_cast<float2*>(base + ws.chunk_ml);
     c.part_o = reinterpret_cast<float*>(base + ws.chunk_o);
-    if (!(codes ? launch_chunks<true>(c, d, k_cache, v_cache, split, st_)
-                : launch_chunks<false>(c, d, k_cache, v_cache, split, st_)))
+    if (!(codes ? launch_chunks<true>(c, d, k_cache, v_cache, split, &chunk_join, st_)
+                : launch_chunks<false>(c, d, k_cache, v_cache, split, &chunk_join, st_)))
       return SINK_ATTN_ERR_CUDA;
   }
-  if (split.rows && !(codes ? launch_rows<true>(split.kR, p, d, k_cache, v_cache, st_)
-                            : launch_rows<false>(split.kR, p, d, k_cache, v_cache, st_)))
+  if (split.rows && !(codes ? launch_rows<true>(split.kR, p, d, k_cache, v_cache, split.chunks, &rows_join, st_)
+                            : launch_rows<false>(split.kR, p, d, k_cache, v_cache, split.chunks, &rows_join, st_)))
+    return SINK_ATTN_ERR_CUDA;
+  if (chunk_join.x && !launch_early(codes ? sink_attn_paged_chunk_join_kernel<true> : sink_attn_paged_chunk_join_kernel<false>,
+                                    chunk_join, 256, 0, st_, c))
+    return SINK_ATTN_ERR_CUDA;
+  if (rows_join.x && !launch_early(split.kR == 8 ? sink_attn_paged_join_kernel<8> : sink_attn_paged_join_kernel<16>,
+                                   rows_join, 256, 0, st_, p))
     return SINK_ATTN_ERR_CUDA;
   return SINK_ATTN_OK;
 }
