@@ -69,12 +69,16 @@ void check(const Tensor& t, const char* name, at::ScalarType type, std::initiali
   if (!fine) refuse(t, name, type, at::IntArrayRef(shape.begin(), shape.size()), device, strides);
 }
 
+// The stride of a dimension; of one with a single element, which no address
+// needs, any multiple of a row.
+int64_t stride_of(const Tensor& t, int dim) { return t.size(dim) > 1 ? t.stride(dim) : kHeadDim; }
+
 // bf16 [T][heads][64] whose tokens are contiguous; returns the token stride.
 int64_t check_heads(const Tensor& t, const char* name, int64_t tokens, int64_t heads, int device) {
   check(t, name, at::kBFloat16, {tokens, heads, kHeadDim}, device, true);
   if (t.stride(2) != 1 || (heads > 1 && t.stride(1) != kHeadDim))
     throw Refused(std::string(name) + ": the heads of a token are not contiguous");
-  return t.stride(0);
+  return stride_of(t, 0);
 }
 
 int as_int(int64_t v, const char* name) {
@@ -135,7 +139,9 @@ Cache cache_of(const Args& a, int k, int v, int ks, int vs) {
   check(*c.k, "k_cache", type, {kAny, kAny, kAny, kHeadDim}, c.device, true);
   c.pages = c.k->size(0), c.page = c.k->size(1), c.heads = c.k->size(2);
   check(*c.v, "v_cache", type, {c.pages, c.page, c.heads, kHeadDim}, c.device, true);
-  if (c.k->strides() != c.v->strides() || c.k->stride(3) != 1)
+  bool same = c.k->stride(3) == 1 && c.v->stride(3) == 1;
+  for (int i = 0; i < 3; ++i) same = same && stride_of(*c.k, i) == stride_of(*c.v, i);
+  if (!same)
     throw Refused("k_cache and v_cache need the same strides, with contiguous rows");
   c.k_scale = c.v_scale = nullptr;
   if (c.codes) {
@@ -155,9 +161,9 @@ void fill(sink_attn_paged_dims* d, const Cache& c) {
   d->head_dim = kHeadDim;
   d->page_size = as_int(c.page, "page_size");
   d->num_pages = as_int(c.pages, "num_pages");
-  d->page_stride = c.k->stride(0);
-  d->token_stride = c.k->stride(1);
-  d->head_stride = c.k->stride(2);
+  d->page_stride = stride_of(*c.k, 0);
+  d->token_stride = stride_of(*c.k, 1);
+  d->head_stride = stride_of(*c.k, 2);
 }
 
 // The C call, with the interpreter free for other threads.

@@ -598,6 +598,14 @@ sink_attn_status check_paged(const sink_attn_paged_dims* d, bool codes) {
   if (static_cast<int64_t>(d->num_pages) * d->page_size >= (int64_t(1) << 31) ||
       d->total_tokens > (1 << 30) || d->num_kv_heads > (1 << 16))
     return SINK_ATTN_ERR_UNSUPPORTED;
+  // Rows of a cache do not overlap (a dimension of one element may have any
+  // stride), and TMA takes strides below 2^40 bytes.
+  const long long strides[3] = {d->page_stride, d->token_stride, d->head_stride};
+  const int sizes[3] = {d->num_pages, d->page_size, d->num_kv_heads};
+  for (int i = 0; i < 3; ++i) {
+    if (sizes[i] > 1 && strides[i] < kHeadDim) return SINK_ATTN_ERR_SHAPE;
+    if (strides[i] >= (1ll << 38)) return SINK_ATTN_ERR_UNSUPPORTED;
+  }
   const long long unit = codes ? 16 : 8;
   if (d->page_stride % unit || d->token_stride % unit || d->head_stride % unit) return SINK_ATTN_ERR_ALIGN;
   return SINK_ATTN_OK;
@@ -655,6 +663,8 @@ sink_attn_status check_paged_attn(const sink_attn_paged_dims* d, bool codes) {
   const int64_t chunks = d->num_kv_heads;  // of heads, at most
   if (tokens > (int64_t(1) << 30) || tokens * std::max(d->batch, 1) > (int64_t(1) << 35) / chunks)
     return SINK_ATTN_ERR_UNSUPPORTED;
+  if (d->total_tokens > 1 && d->q_stride < static_cast<long long>(d->num_q_heads) * kHeadDim) return SINK_ATTN_ERR_SHAPE;
+  if (d->q_stride >= (1ll << 38)) return SINK_ATTN_ERR_UNSUPPORTED;
   if (d->q_stride % 8) return SINK_ATTN_ERR_ALIGN;
   return SINK_ATTN_OK;
 }
@@ -910,7 +920,8 @@ sink_attn_status paged_attn_impl(const sink_attn_paged_dims* d, const void* q, c
   p.row_parts = split.row_parts;
   p.chunks = rows_chunks(d, split);
   p.per_chunk = (p.Hkv + p.chunks - 1) / p.chunks;
-  p.window = window > 0 ? window : 0;
+  // (A window beyond all positions is none, and keeps their differences in 32 bits.)
+  p.window = window > 0 && window < (1 << 30) ? window : 0;
   p.scale_log2 = scale * kLog2e;
   p.q_stride = d->q_stride;
   p.q = static_cast<const __nv_bfloat16*>(q);
