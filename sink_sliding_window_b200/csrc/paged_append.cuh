@@ -25,13 +25,15 @@ struct AppendParams {
 template <bool kF8>
 __global__ void __launch_bounds__(256) sink_attn_paged_append_kernel(const AppendParams p) {
   constexpr int kChunks = kHeadDim / 16;
+  pdl_launch_dependents();
+  pdl_wait();
   const long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
   const int per = p.Hkv * kChunks;
   const long long t = i / per;
   if (t >= p.tokens) return;
   const int r = static_cast<int>(i - t * per);
   const int g = r / kChunks, c = r % kChunks;
-  const int slot = __ldg(p.slots + t);
+  const int slot = *(p.slots + t);
   if (slot < 0) return;  // padding, or a request without room
   if (slot >= p.slots_end) {
     atomicCAS(&g_device_error, 0, static_cast<int>(kDevErrBadPage));
@@ -39,11 +41,11 @@ __global__ void __launch_bounds__(256) sink_attn_paged_append_kernel(const Appen
   }
   const uint4* ks = reinterpret_cast<const uint4*>(p.k_new + t * p.k_stride + g * kHeadDim + c * 16);
   const uint4* vs = reinterpret_cast<const uint4*>(p.v_new + t * p.v_stride + g * kHeadDim + c * 16);
-  const uint4 k0 = __ldg(ks), k1 = __ldg(ks + 1), v0 = __ldg(vs), v1 = __ldg(vs + 1);
+  const uint4 k0 = *(ks), k1 = *(ks + 1), v0 = *(vs), v1 = *(vs + 1);
   const long long dst = (slot >> p.page_log2) * p.page_stride +
                         (slot & ((1 << p.page_log2) - 1)) * p.token_stride + g * p.head_stride + c * 16;
   if constexpr (kF8) {
-    const float ki = 1.f / __ldg(p.k_scale + g), vi = 1.f / __ldg(p.v_scale + g);
+    const float ki = 1.f / *(p.k_scale + g), vi = 1.f / *(p.v_scale + g);
     const uint32_t kin[8] = {k0.x, k0.y, k0.z, k0.w, k1.x, k1.y, k1.z, k1.w};
     const uint32_t vin[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
     uint32_t kw[8], vw[8];

@@ -13,6 +13,7 @@ struct PagedParams {
   int page_log2, num_pages, max_pages;
   int box_log2;      // tokens of one TMA box of the few-rows kernel
   int few;           // a request of at most this many new tokens goes to the few-rows kernel
+  bool beside;       // few-rows kernel: the chunk kernel runs before it on the stream
   int window;        // 0: full causal
   float scale_log2;  // scale * log2(e)
   long long q_stride;
@@ -36,6 +37,10 @@ struct PagedParams {
   int4* part_unit;   // [workers] (b or -1, chunk, begins, 0)
 };
 
+// All loads of a call's inputs are plain ones: the kernels may start while the
+// ones before them still write (see pdl_wait), which rules out the read-only
+// path.
+
 // One request's rows and keys.  Lengths that do not fit the call's sizes are
 // cut to them (and reported by paged_check), so that no index leaves a tensor.
 struct PagedRequest {
@@ -46,23 +51,23 @@ struct PagedRequest {
 
 __device__ __forceinline__ PagedRequest paged_request(const PagedParams& p, int b) {
   PagedRequest r;
-  r.t0 = min(max(__ldg(p.cu + b), 0), p.T);
-  r.n = min(max(__ldg(p.cu + b + 1), r.t0), p.T) - r.t0;
-  r.len = min(max(__ldg(p.kv_lens + b), 0), p.max_pages << p.page_log2);
+  r.t0 = min(max(*(p.cu + b), 0), p.T);
+  r.n = min(max(*(p.cu + b + 1), r.t0), p.T) - r.t0;
+  r.len = min(max(*(p.kv_lens + b), 0), p.max_pages << p.page_log2);
   r.lo = p.window > 0 ? max(0, r.len - r.n - p.window + 1) : 0;
   return r;
 }
 
 // Reports a request whose lengths do not fit.
 __device__ __forceinline__ void paged_check(const PagedParams& p, int b) {
-  const int c0 = __ldg(p.cu + b), c1 = __ldg(p.cu + b + 1), len = __ldg(p.kv_lens + b);
+  const int c0 = *(p.cu + b), c1 = *(p.cu + b + 1), len = *(p.kv_lens + b);
   if (c0 < 0 || c1 < c0 || c1 > p.T || c1 - c0 > p.max_new || len < 0 || len > (p.max_pages << p.page_log2))
     atomicCAS(&g_device_error, 0, static_cast<int>(kDevErrPagedRows));
 }
 
 // The table's entry for the page that holds key j of request b.
 __device__ __forceinline__ int paged_entry(const PagedParams& p, int b, int j) {
-  return __ldg(p.table + static_cast<long long>(b) * p.max_pages + (j >> p.page_log2));
+  return *(p.table + static_cast<long long>(b) * p.max_pages + (j >> p.page_log2));
 }
 
 // A table entry as a page: num_pages, which a TMA load reads as zeros, when it
@@ -82,10 +87,5 @@ __device__ __forceinline__ void tma_load_4d(void* smem_dst, const CUtensorMap* m
       "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "r"(w)
       : "memory");
 }
-
-// Programmatic dependent launch: lets the next kernel of the stream start, and
-// waits until the kernels before this one have completed.
-__device__ __forceinline__ void pdl_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 }  // namespace sa

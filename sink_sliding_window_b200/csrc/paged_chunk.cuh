@@ -166,6 +166,8 @@ __global__ void __launch_bounds__(kChunkThreads<kF8>, kChunkPerSm<kF8>)
   auto* ctl = reinterpret_cast<ChunkCtl<kF8>*>(sB + (kF8 ? kChunkSlots * kChunkSlotBytes : 0));
   volatile int* abort = &ctl->abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // In this order: the few-rows kernel beside this one does not wait again.
+  pdl_wait();
   pdl_launch_dependents();
 
   // -------------------------------------------------------- the units of the call
@@ -453,10 +455,10 @@ __global__ void __launch_bounds__(kChunkThreads<kF8>, kChunkPerSm<kF8>)
       const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
       const uint32_t tS = tmem + lane_base + wg * kHalfN;
       const uint32_t tO = tmem + lane_base + kTmemO + wg * kHeadDim;
-      const float sl2 = kF8 ? p.a.scale_log2 * __ldg(p.a.k_scale + g) : p.a.scale_log2;
+      const float sl2 = kF8 ? p.a.scale_log2 * *(p.a.k_scale + g) : p.a.scale_log2;
       // A part of a unit with fewer key tiles than parts may have none.
       bool ok = n_half > 0 && wg < live;
-      const float s2 = valid ? __ldg(p.a.sinks + h) * kLog2e : 0.f;
+      const float s2 = valid ? *(p.a.sinks + h) * kLog2e : 0.f;
       if constexpr (kF8) {
         if (n_half > 0 && wg >= live) mbar_arrive(&ctl->q_conv);
         ok = ok && warp_all(mbar_wait(&ctl->q_full, 0, abort, &g_device_error, kDevErrTimeoutSoftmax));
@@ -532,7 +534,7 @@ __global__ void __launch_bounds__(kChunkThreads<kF8>, kChunkPerSm<kF8>)
         uint32_t o[kHeadDim];
         __syncwarp();
         tmem_ld64(tO, o);
-        const float vs = kF8 ? __ldg(p.a.v_scale + g) : 1.f;
+        const float vs = kF8 ? *(p.a.v_scale + g) : 1.f;
         if (parts > 1) {
           const long long at = static_cast<long long>(slot) * kTiles * kBlockM + wg * kBlockM + r;
           p.part_ml[at] = make_float2(m_ref, l);
@@ -597,7 +599,7 @@ __global__ void __launch_bounds__(256) sink_attn_paged_chunk_join_kernel(const _
     const int it = (kTiles * u.y + (row >> 7)) * p.tokens + row_t;
     if (row_t >= p.tokens || it >= rq.n) continue;
     const int h = u.z * p.a.G + r - row_t * p.a.G;
-    const float s2 = __ldg(p.a.sinks + h) * kLog2e;
+    const float s2 = *(p.a.sinks + h) * kLog2e;
     float m = -INFINITY, l = 0.f;
     float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4

@@ -67,6 +67,8 @@ __device__ __forceinline__ int plan_find(const int* v, int n, int x) {
 }
 
 __global__ void __launch_bounds__(kPlanThreads) sink_attn_paged_plan_kernel(const PlanParams p) {
+  pdl_launch_dependents();
+  pdl_wait();
   extern __shared__ int plan_smem[];
   int* s_cu = plan_smem;                  // [batch + 1]
   int* s_rel = s_cu + p.batch + 1;        // [batch + 1]
@@ -77,9 +79,9 @@ __global__ void __launch_bounds__(kPlanThreads) sink_attn_paged_plan_kernel(cons
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t most = static_cast<int64_t>(p.max_pages) << p.page_log2;  // tokens a table row covers
   const int num = p.num_pages;
-  int head = __ldg(p.pool) % num;
+  int head = *(p.pool) % num;
   if (head < 0) head += num;
-  const int count = min(max(__ldg(p.pool + 1), 0), num);
+  const int count = min(max(*(p.pool + 1), 0), num);
 
   // Each thread owns `items` neighbouring requests.
   const int items = (p.batch + kPlanThreads - 1) / kPlanThreads;

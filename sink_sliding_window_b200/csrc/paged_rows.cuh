@@ -67,7 +67,7 @@ struct RowsCtl {
   uint64_t full[kRowsWarps * kRowsMaxStages];   // [worker of the CTA][stage]
   uint64_t empty[kRowsWarps * kRowsMaxStages];
   int abort;
-  int sums[kRowsWarps + 1];
+  int sums[kRowsWarps + 1], live[kRowsWarps + 1];
   int4 cuts[kRowsWarps][2];  // where the pieces of the CTA's workers begin and end: x, b, c, off
 };
 
@@ -188,7 +188,6 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
   int* pre = reinterpret_cast<int*>(ctl + 1);
   volatile int* abort = &ctl->abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  pdl_launch_dependents();  // the joins wait for this kernel's end by themselves
 
   const int per_group = p.per_chunk * p.row_parts;  // warps of a worker
   const int groups = kWarps / per_group;             // workers of this CTA
@@ -203,11 +202,15 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
   }
+  // The call's inputs and the workspace are free to use; beside the chunk
+  // kernel they are already, since that waited before it let this one start.
+  if (!p.beside) pdl_wait();
+  pdl_launch_dependents();
   // pre[]: every CTA sums the requests' blocks for itself.
   {
     const int per = (p.batch + kThreads - 1) / kThreads;
     const int b0 = threadIdx.x * per;
-    int sum = 0;
+    int sum = 0, live = 0;  // blocks, requests that have some
     for (int i = 0; i < per; ++i) {
       const int b = b0 + i;
       if (b >= p.batch) break;
@@ -215,6 +218,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
       const int n = rows_blocks<kF8>(p, paged_request(p, b));
       pre[b + 1] = n;
       sum += n;
+      live += n > 0;
     }
     int in = sum;
 #pragma unroll
@@ -222,7 +226,8 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
       const int v = __shfl_up_sync(0xffffffffu, in, o);
       if (lane >= o) in += v;
     }
-    if (lane == 31) ctl->sums[warp] = in;
+    live = __reduce_add_sync(0xffffffffu, live);
+    if (lane == 31) ctl->sums[warp] = in, ctl->live[warp] = live;
     __syncthreads();
     int at = in - sum;
     for (int w = 0; w < warp; ++w) at += ctl->sums[w];
@@ -241,7 +246,10 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
   axis.batch = p.batch;
   axis.chunks = p.chunks;
   axis.total = static_cast<uint32_t>(pre[p.batch]) * p.chunks;
-  axis.workers = min(gridDim.x * groups, (axis.total + kRowsMinBlocks - 1) / kRowsMinBlocks);
+  uint32_t units = 0;
+  for (int w = 0; w <= kWarps; ++w) units += ctl->live[w];
+  // (A worker for each unit at least: short ones are not cut.)
+  axis.workers = min(gridDim.x * groups, max(units * p.chunks, (axis.total + kRowsMinBlocks - 1) / kRowsMinBlocks));
 
   // Worker g of this CTA: consecutive pieces go to different SMs, so that a few
   // of them do not share one.
@@ -377,7 +385,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
       whole = at.off == 0;
       g = min(at.c * p.per_chunk + hw, p.Hkv - 1);
       real = at.c * p.per_chunk + hw < p.Hkv;
-      sl2 = kF8 ? p.scale_log2 * __ldg(p.k_scale + g) : p.scale_log2;
+      sl2 = kF8 ? p.scale_log2 * *(p.k_scale + g) : p.scale_log2;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         m[h] = -INFINITY;
@@ -393,12 +401,12 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
           uint32_t a = 0u, c = 0u;
           if (h < kHalves && t < rq.n) {
             if constexpr (kF8) {
-              const uint2 v = __ldg(reinterpret_cast<const uint2*>(src + 16 * kk + 4 * t4));
+              const uint2 v = *(reinterpret_cast<const uint2*>(src + 16 * kk + 4 * t4));
               a = bf16x2_to_f16x2_sat(v.x);
               c = bf16x2_to_f16x2_sat(v.y);
             } else {
-              a = __ldg(reinterpret_cast<const uint32_t*>(src + 16 * kk + 2 * t4));
-              c = __ldg(reinterpret_cast<const uint32_t*>(src + 16 * kk + 8 + 2 * t4));
+              a = *(reinterpret_cast<const uint32_t*>(src + 16 * kk + 2 * t4));
+              c = *(reinterpret_cast<const uint32_t*>(src + 16 * kk + 8 + 2 * t4));
             }
           }
           q[kk][h] = a;
@@ -542,7 +550,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
       const bool begun = whole;
       whole = whole && unit_end;
       const int slot = (2 * worker + (unit_end ? 0 : 1)) * per_group + in_group;
-      const float vs = kF8 ? __ldg(p.v_scale + g) : 1.f;
+      const float vs = kF8 ? *(p.v_scale + g) : 1.f;
 #pragma unroll
       for (int h = 0; h < kHalves; ++h) {
         const int row = row0 + 8 * h + r8;
@@ -554,7 +562,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
         const int head = valid ? g * p.G + row - t * p.G : 0;
         float f = vs;
         if (whole) {
-          const float s2 = __ldg(p.sinks + head) * kLog2e;
+          const float s2 = *(p.sinks + head) * kLog2e;
           const float top = fmaxf(s2, m[h]);
           float all = 0.f;
           f = 0.f;
@@ -633,6 +641,7 @@ __global__ void __launch_bounds__(256, kR == 8 ? 3 : 2) sink_attn_paged_join_ker
   __shared__ float s_o[8][8][kHeadDim];
   __shared__ float s_m[8][8], s_l[8][8];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  pdl_launch_dependents();
   pdl_wait();
   // The first piece is that of the nearest worker before this one whose last
   // piece begins a request: one load per lane tells for 31 of them.
@@ -657,7 +666,7 @@ __global__ void __launch_bounds__(256, kR == 8 ? 3 : 2) sink_attn_paged_join_ker
   do {
     const int row = row0 + r0 + warp, t = row / p.G;  // this warp's row in the end
     const int head = g * p.G + row - t * p.G;
-    const float s2 = __ldg(p.sinks + min(head, p.Hq - 1)) * kLog2e;
+    const float s2 = *(p.sinks + min(head, p.Hq - 1)) * kLog2e;
     // This lane's rows r0 + (lane >> 4) + 2 u, u < 4, and dims 4 (lane & 15) ..; a
     // piece's rows behind the last one are in the workspace, and never used.
     float m[4], l[4];

@@ -585,6 +585,25 @@ namespace {
 
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
+// Launches a kernel that may start before the one before it on the stream has
+// ended, and waits for that by itself before it touches memory (pdl_wait): the
+// kernels of a serving step follow one another within a few microseconds, and
+// this hides the start of each.
+template <typename... A>
+bool launch_early(void (*kernel)(A...), dim3 grid, unsigned threads, size_t smem, cudaStream_t st, const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess;
+}
+
 // Sizes and strides shared by the paged append and attention.  `codes`: the
 // cache holds one byte per element, so a row's 16-byte alignment needs strides
 // that are multiples of 16 elements, not 8.
@@ -645,9 +664,10 @@ sink_attn_status paged_append_impl(const sink_attn_paged_dims* d, const void* k_
   const long long blocks = (work + 255) / 256;
   if (blocks > 0x7fffffff) return SINK_ATTN_ERR_UNSUPPORTED;
   cudaStream_t st_ = static_cast<cudaStream_t>(stream);
-  if (codes) sink_attn_paged_append_kernel<true><<<static_cast<unsigned>(blocks), 256, 0, st_>>>(p);
-  else sink_attn_paged_append_kernel<false><<<static_cast<unsigned>(blocks), 256, 0, st_>>>(p);
-  return cudaPeekAtLastError() == cudaSuccess ? SINK_ATTN_OK : SINK_ATTN_ERR_CUDA;
+  return launch_early(codes ? sink_attn_paged_append_kernel<true> : sink_attn_paged_append_kernel<false>,
+                      dim3(static_cast<unsigned>(blocks)), 256, 0, st_, p)
+             ? SINK_ATTN_OK
+             : SINK_ATTN_ERR_CUDA;
 }
 
 sink_attn_status check_paged_attn(const sink_attn_paged_dims* d, bool codes) {
@@ -782,26 +802,10 @@ bool make_map_paged(CUtensorMap* map, const void* base, const sink_attn_paged_di
 // inside one (see RowsAxis::cut): nothing to join.
 template <bool kF8>
 bool rows_never_cut(const PagedParams& p) {
-  const int64_t keys = p.window > 0 ? static_cast<int64_t>(p.window) + p.few - 1 : int64_t(p.max_pages) << p.page_log2;
+  const int64_t keys = std::min(int64_t(p.max_pages) << p.page_log2,
+                                p.window > 0 ? static_cast<int64_t>(p.window) + p.few - 1 : INT64_MAX);
   const int64_t lead = p.window > 0 ? (1 << p.box_log2) - 1 : 0;
   return (keys + lead + kRowsKeys<kF8> - 1) / kRowsKeys<kF8> <= 2 * kRowsSnap<kF8> + 1;
-}
-
-// Launches a kernel that may start before the one before it on the stream has
-// ended, and waits for that (griddepcontrol.wait) where it needs to.
-template <typename... A>
-bool launch_early(void (*kernel)(A...), dim3 grid, unsigned threads, size_t smem, cudaStream_t st, const A&... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads, 1, 1);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess;
 }
 
 // `beside`: the chunk kernel runs before it on the stream.  The two share
@@ -822,15 +826,14 @@ bool launch_rows(PagedParams& p, const sink_attn_paged_dims* d, const void* k_ca
   // No more CTAs than the most blocks there can be give work to.
   const int64_t keys = p.window > 0 ? static_cast<int64_t>(p.window) + p.few - 1 + box : INT64_MAX;
   const int64_t most = (std::min(keys, int64_t(p.max_pages) << p.page_log2) + kRowsKeys<kF8> - 1) / kRowsKeys<kF8> + 1;
-  const int64_t workers = (most * p.batch * p.chunks + kRowsMinBlocks - 1) / kRowsMinBlocks;
+  const int64_t workers = std::max((most * p.batch * p.chunks + kRowsMinBlocks - 1) / kRowsMinBlocks,
+                                   int64_t(p.batch) * p.chunks);
   const int per_group = p.per_chunk * p.row_parts, groups = kRowsWarps / per_group;
   const int ctas = static_cast<int>(std::min<int64_t>(kPagedCtas, workers));
   if (cut) *join = dim3(ctas * groups, per_group);
-  if (beside)
-    return launch_early(sink_attn_paged_rows_kernel<kF8, kR>, dim3(ctas), kRowsThreads, rows_smem_bytes(p.batch), st, tm_k,
-                        tm_v, p);
-  sink_attn_paged_rows_kernel<kF8, kR><<<ctas, kRowsThreads, rows_smem_bytes(p.batch), st>>>(tm_k, tm_v, p);
-  return cudaPeekAtLastError() == cudaSuccess;
+  p.beside = beside;
+  return launch_early(sink_attn_paged_rows_kernel<kF8, kR>, dim3(ctas), kRowsThreads, rows_smem_bytes(p.batch), st, tm_k,
+                      tm_v, p);
 }
 
 template <bool kF8>
@@ -880,9 +883,9 @@ bool launch_chunks(ChunkParams& p, const sink_attn_paged_dims* d, const void* k_
   const bool turns = bound.parts == 0 || d->total_tokens < static_cast<int64_t>(d->batch) * d->max_new / 2;
   const int64_t places = bound.units + bound.parts;
   const unsigned ctas = static_cast<unsigned>(std::min<int64_t>(places, (turns ? 1 : kChunkMaxWaves + 1) * p.wave));
-  sink_attn_paged_chunk_kernel<kF8><<<ctas, kChunkThreads<kF8>, chunk_smem_bytes<kF8>(), st>>>(tm_q, tm_k, tm_v, p);
   if (bound.parts) *join = dim3(static_cast<unsigned>(std::min<int64_t>(bound.units, p.wave - 1)), kChunkTiles<kF8> * kBlockM / 32);
-  return cudaPeekAtLastError() == cudaSuccess;
+  return launch_early(sink_attn_paged_chunk_kernel<kF8>, dim3(ctas), kChunkThreads<kF8>, chunk_smem_bytes<kF8>(), st, tm_q,
+                      tm_k, tm_v, p);
 }
 
 sink_attn_status paged_attn_impl(const sink_attn_paged_dims* d, const void* q, const void* k_cache,
@@ -917,6 +920,7 @@ sink_attn_status paged_attn_impl(const sink_attn_paged_dims* d, const void* q, c
   p.max_pages = d->max_pages;
   p.box_log2 = 0;
   p.few = split.few;
+  p.beside = false;
   p.row_parts = split.row_parts;
   p.chunks = rows_chunks(d, split);
   p.per_chunk = (p.Hkv + p.chunks - 1) / p.chunks;
@@ -1020,13 +1024,15 @@ sink_attn_status sink_attn_paged_plan(const sink_attn_plan_dims* d, const int* c
   cfg.blockDim = dim3(kPlanThreads, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = static_cast<cudaStream_t>(stream);
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = blocks;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // see launch_early
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, sink_attn_paged_plan_kernel, p) == cudaSuccess ? SINK_ATTN_OK : SINK_ATTN_ERR_CUDA;
 }
 
