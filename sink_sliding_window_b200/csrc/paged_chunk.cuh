@@ -47,6 +47,8 @@ constexpr int kChunkPerSm = kF8 ? 1 : 2;
 constexpr int kChunkSms = 148;
 constexpr int kChunkMaxWaves = 3;  // of parts
 constexpr int kChunkFixed = 8;     // a part's set-up, ends and join, in 64-key steps
+constexpr int kChunkLeast = 4;     // steps of a part
+constexpr int kChunkMostParts = 32;  // of a unit
 constexpr int kChunkSlots = 4;
 constexpr int kChunkSlotKeys = 64;
 constexpr int kChunkSlotBytes = kChunkSlotKeys * kHeadDim;  // e4m3 codes of K or V
@@ -111,7 +113,7 @@ __device__ __forceinline__ int chunk_parts(int rest, int steps, int wave) {
   for (int w = 1; w <= kChunkMaxWaves; ++w) {
     int k = static_cast<int>(__fdividef(static_cast<float>(w * wave), static_cast<float>(rest)) + 0.01f);
     if (k * rest > w * wave) --k;
-    k = min(k, steps / kChunkFixed);
+    k = min(min(k, steps / kChunkLeast), kChunkMostParts);
     const float cost = w * (__fdividef(static_cast<float>(steps), static_cast<float>(k)) + 2 * kChunkFixed);
     if (k >= 2 && cost < least) least = cost, best = k;
   }
@@ -352,16 +354,13 @@ __global__ void __launch_bounds__(kChunkThreads<kF8>, kChunkPerSm<kF8>)
             mbar_arrive_expect_tx(&ctl->v_full[s], kTileBytes);
           }
           __syncwarp();
-          for (int y = 0; y < 2 * nbox; ++y) {  // K first: S waits for it
-            const bool is_v = y >= nbox;
-            const int x = is_v ? y - nbox : y;
-            const int page = __shfl_sync(0xffffffffu, mine, x);
-            const int at = (key0 + j * kBlockN + (x << box_log2)) & page_mask;
-            if (elect_one())
-              tma_load_4d((is_v ? sV : sK) + s * kTileBytes + (x << box_log2) * kHeadDim * 2, is_v ? &tm_v : &tm_k,
-                          is_v ? &ctl->v_full[s] : &ctl->k_full[s], 0, at, g, page);
-            __syncwarp();
+          if (lane < nbox) {  // K first: S waits for it
+            const int at = (key0 + j * kBlockN + (lane << box_log2)) & page_mask;
+            const int to = s * kTileBytes + (lane << box_log2) * kHeadDim * 2;
+            tma_load_4d(sK + to, &tm_k, &ctl->k_full[s], 0, at, g, mine);
+            tma_load_4d(sV + to, &tm_v, &ctl->v_full[s], 0, at, g, mine);
           }
+          __syncwarp();
         }
       } else if (kF8 && warp == kCopyWarp) {
         // ------------------------------------------------------ e4m3: TMA producer
@@ -386,14 +385,12 @@ __global__ void __launch_bounds__(kChunkThreads<kF8>, kChunkPerSm<kF8>)
           uint8_t* to = sB + at_slot * kChunkSlotBytes;
           if (elect_one()) mbar_arrive_expect_tx(full, kChunkSlotBytes);
           __syncwarp();
-          for (int x = 0; x < per_slot; ++x) {
-            const int box = (e & 1) * per_slot + x;
-            const int page = __shfl_sync(0xffffffffu, mine, box);
-            const int at = (key0 + j * kBlockN + (box << box_log2)) & page_mask;
-            if (elect_one())
-              tma_load_4d(to + (x << box_log2) * kHeadDim, e < 2 ? &tm_k : &tm_v, full, 0, at, g, page);
-            __syncwarp();
+          const int x = lane - (e & 1) * per_slot;
+          if (x >= 0 && x < per_slot) {
+            const int at = (key0 + j * kBlockN + (lane << box_log2)) & page_mask;
+            tma_load_4d(to + (x << box_log2) * kHeadDim, e < 2 ? &tm_k : &tm_v, full, 0, at, g, mine);
           }
+          __syncwarp();
         }
       } else if (kF8) {
         // ------------------------------------------------------------ e4m3: widen
@@ -602,7 +599,7 @@ __global__ void __launch_bounds__(256) sink_attn_paged_chunk_join_kernel(const _
     const float s2 = *(p.a.sinks + h) * kLog2e;
     float m = -INFINITY, l = 0.f;
     float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
+#pragma unroll 8
     for (int k = 0; k < u.w; ++k) {
       const long long at = (static_cast<long long>(i) * u.w + k) * kTiles * kBlockM + row;
       const float2 ml = __ldcg(p.part_ml + at);

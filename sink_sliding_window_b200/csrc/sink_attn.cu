@@ -734,7 +734,7 @@ ChunkBound chunk_bound(const sink_attn_paged_dims* d, const PagedSplit& s, int w
   c.units = d->num_kv_heads * (d->total_tokens / tokens + requests);
   const int64_t keys = std::min<int64_t>(int64_t(d->max_pages) * d->page_size,
                                          window > 0 ? int64_t(window) + tokens : INT64_MAX);
-  const int64_t most = (keys / kHalfN + 1) / kChunkFixed;  // parts of a unit
+  const int64_t most = std::min<int64_t>((keys / kHalfN + 1) / kChunkLeast, kChunkMostParts);  // parts of a unit
   const int64_t wave = kChunkPerSm<kF8> * kChunkSms;
   c.parts = most < 2 ? 0 : std::min(kChunkMaxWaves * wave, std::min(c.units, wave) * most);
   return c;
