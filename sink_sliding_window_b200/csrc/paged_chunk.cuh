@@ -57,6 +57,7 @@ struct ChunkParams {
   PagedParams a;
   int tokens;          // P: tokens of a query tile
   int wave;            // CTAs that run at once
+  int tiles;           // kTiles
   float* part_o;       // [part][kTiles * 128 rows][64]
   float2* part_ml;     // [part][kTiles * 128] (m in log2 units, l)
   int4* part_unit;     // [cut unit] (request, unit within its head, head, parts)
@@ -575,54 +576,6 @@ __global__ void __launch_bounds__(kChunkThreads<kF8>, kChunkPerSm<kF8>)
 
   __syncthreads();
   if (warp == kMmaWarp) tmem_dealloc(ctl->tmem_base, 2 * kTmemO);
-}
-
-// Joins the parts of the cut units and adds the sink.  One CTA per cut unit
-// and 32 of its rows; half a warp per row, four dims per lane.
-template <bool kF8>
-__global__ void __launch_bounds__(256) sink_attn_paged_chunk_join_kernel(const __grid_constant__ ChunkParams p) {
-  pdl_launch_dependents();
-  pdl_wait();
-  const int i = blockIdx.x;
-  if (i >= __ldcg(p.part_units)) return;
-  const int4 u = __ldcg(p.part_unit + i);
-  const PagedRequest rq = paged_request(p.a, u.x);
-  constexpr int kTiles = kChunkTiles<kF8>;
-  const int d = threadIdx.x & 15;
-#pragma unroll
-  for (int x = 0; x < 2; ++x) {
-    const int row = blockIdx.y * 32 + x * 16 + (threadIdx.x >> 4);
-    const int r = row & (kBlockM - 1), row_t = r / p.a.G;
-    const int it = (kTiles * u.y + (row >> 7)) * p.tokens + row_t;
-    if (row_t >= p.tokens || it >= rq.n) continue;
-    const int h = u.z * p.a.G + r - row_t * p.a.G;
-    const float s2 = *(p.a.sinks + h) * kLog2e;
-    float m = -INFINITY, l = 0.f;
-    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-    for (int k = 0; k < u.w; ++k) {
-      const long long at = (static_cast<long long>(i) * u.w + k) * kTiles * kBlockM + row;
-      const float2 ml = __ldcg(p.part_ml + at);
-      const float4 v = __ldcg(reinterpret_cast<const float4*>(p.part_o + at * kHeadDim) + d);
-      const float now = fmaxf(m, ml.x);
-      if (ml.x == -INFINITY) continue;  // a part of no keys, or of none that the row sees
-      const float f0 = ex2_approx(m - now), f1 = ex2_approx(ml.x - now);
-      m = now;
-      l = l * f0 + ml.y * f1;
-      y = make_float4(y.x * f0 + v.x * f1, y.y * f0 + v.y * f1, y.z * f0 + v.z * f1, y.w * f0 + v.w * f1);
-    }
-    const float top = fmaxf(m, s2);
-    float f = 0.f, all = 0.f;
-    if (top != -INFINITY) {
-      f = ex2_approx(m - top);
-      all = fmaf(l, f, s2 == top ? 1.f : ex2_approx(s2 - top));
-    }
-    f = all > 0.f ? f / all : 0.f;
-    const int t = rq.t0 + it;
-    *reinterpret_cast<uint2*>(p.a.out + (static_cast<long long>(t) * p.a.Hq + h) * kHeadDim + 4 * d) =
-        make_uint2(pack_bf16x2(y.x * f, y.y * f), pack_bf16x2(y.z * f, y.w * f));
-    if (d == 0) p.a.lse[static_cast<long long>(h) * p.a.T + t] = all > 0.f ? (top + __log2f(all)) * kLn2 : -INFINITY;
-  }
 }
 
 }  // namespace sa

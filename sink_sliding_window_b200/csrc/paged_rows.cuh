@@ -630,121 +630,4 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
   if (reports) p.part_unit[worker] = unit;
 }
 
-// Joins the pieces of every cut request and adds the sink: with M = max(s, max_k m_k),
-//   l = e^{s-M} + sum_k l_k e^{m_k-M},  out = sum_k O_k e^{m_k-M} / l,  lse = M + ln l.
-// One CTA per worker and warp of a worker, whose work is the request that the
-// worker completed (mostly none).  Its warps take the pieces in turn, eight
-// rows at a time (a lane holds four rows' four dims), then join their own
-// eight results in shared memory in the same way.
-template <int kR>
-__global__ void __launch_bounds__(256, kR == 8 ? 3 : 2) sink_attn_paged_join_kernel(const __grid_constant__ PagedParams p) {
-  __shared__ float s_o[8][8][kHeadDim];
-  __shared__ float s_m[8][8], s_l[8][8];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  pdl_launch_dependents();
-  pdl_wait();
-  // The first piece is that of the nearest worker before this one whose last
-  // piece begins a request: one load per lane tells for 31 of them.
-  const int last = blockIdx.x, in_group = blockIdx.y, per_group = p.per_chunk * p.row_parts;
-  const int hw = in_group / p.row_parts, row0 = 16 * (in_group - hw * p.row_parts);
-  const int4 near = __ldcg(p.part_unit + max(last - lane, 0));
-  const int b = __shfl_sync(0xffffffffu, near.x, 0), g = __shfl_sync(0xffffffffu, near.y, 0) * p.per_chunk + hw;
-  if (b < 0 || g >= p.Hkv) return;
-  const PagedRequest rq = paged_request(p, b);
-  uint32_t begins = __ballot_sync(0xffffffffu, lane > 0 && lane <= last && near.z != 0);
-  int start = begins ? last - (__ffs(begins) - 1) : max(0, last - 31);
-  while (begins == 0 && start > 0) {
-    const int w = start - 1 - lane;
-    begins = __ballot_sync(0xffffffffu, w >= 0 && __ldcg(&p.part_unit[max(w, 0)].z) != 0);
-    start = begins ? start - __ffs(begins) : max(0, start - 32);
-  }
-  const int pieces = last - start + 1;
-  auto slot = [&](int k) { return (k + 1 == pieces ? 2 * last : 2 * (start + k) + 1) * per_group + in_group; };
-  // (The first loads wait for neither the request's lengths nor the sinks; a
-  // unit has a row at least.)
-  int r0 = 0;
-  do {
-    const int row = row0 + r0 + warp, t = row / p.G;  // this warp's row in the end
-    const int head = g * p.G + row - t * p.G;
-    const float s2 = *(p.sinks + min(head, p.Hq - 1)) * kLog2e;
-    // This lane's rows r0 + (lane >> 4) + 2 u, u < 4, and dims 4 (lane & 15) ..; a
-    // piece's rows behind the last one are in the workspace, and never used.
-    float m[4], l[4];
-    float4 y[4];
-#pragma unroll
-    for (int u = 0; u < 4; ++u) m[u] = -INFINITY, l[u] = 0.f, y[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-    constexpr int kAtOnce = 2;
-    for (int k0 = warp; k0 < pieces; k0 += 8 * kAtOnce) {
-      float4 v[kAtOnce][4];
-      float2 ml[kAtOnce][4];
-#pragma unroll
-      for (int a = 0; a < kAtOnce; ++a) {
-        const int k = k0 + 8 * a;
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          ml[a][u] = make_float2(-INFINITY, 0.f);
-          if (k < pieces) {
-            const long long at = static_cast<long long>(slot(k)) * kR + r0 + (lane >> 4) + 2 * u;
-            ml[a][u] = __ldcg(p.part_ml + at);
-            v[a][u] = __ldcg(reinterpret_cast<const float4*>(p.part_o + at * kHeadDim) + (lane & 15));
-          } else {
-            v[a][u] = make_float4(0.f, 0.f, 0.f, 0.f);
-          }
-        }
-      }
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        float now = m[u];
-#pragma unroll
-        for (int a = 0; a < kAtOnce; ++a) now = fmaxf(now, ml[a][u].x);
-        const float ref = now == -INFINITY ? 0.f : now;
-        const float f0 = ex2_approx(m[u] - ref);
-        m[u] = now;
-        l[u] *= f0;
-        y[u] = make_float4(y[u].x * f0, y[u].y * f0, y[u].z * f0, y[u].w * f0);
-#pragma unroll
-        for (int a = 0; a < kAtOnce; ++a) {
-          const float f = ex2_approx(ml[a][u].x - ref);
-          l[u] = fmaf(ml[a][u].y, f, l[u]);
-          y[u].x = fmaf(v[a][u].x, f, y[u].x);
-          y[u].y = fmaf(v[a][u].y, f, y[u].y);
-          y[u].z = fmaf(v[a][u].z, f, y[u].z);
-          y[u].w = fmaf(v[a][u].w, f, y[u].w);
-        }
-      }
-    }
-    __syncthreads();  // the last rows have been read
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int r = (lane >> 4) + 2 * u;
-      *reinterpret_cast<float4*>(&s_o[warp][r][4 * (lane & 15)]) = y[u];
-      if ((lane & 15) == 0) s_m[warp][r] = m[u], s_l[warp][r] = l[u];
-    }
-    __syncthreads();
-    // One warp per row, two dims per lane.
-    if (t < rq.n) {
-      float top = s2;
-#pragma unroll
-      for (int w = 0; w < 8; ++w) top = fmaxf(top, s_m[w][warp]);
-      const float ref = top == -INFINITY ? 0.f : top;
-      float all = s2 == ref ? 1.f : ex2_approx(s2 - ref);
-      float2 z = make_float2(0.f, 0.f);
-#pragma unroll
-      for (int w = 0; w < 8; ++w) {
-        const float f = ex2_approx(s_m[w][warp] - ref);
-        const float2 v = *reinterpret_cast<const float2*>(&s_o[w][warp][2 * lane]);
-        all = fmaf(s_l[w][warp], f, all);
-        z.x = fmaf(v.x, f, z.x);
-        z.y = fmaf(v.y, f, z.y);
-      }
-      const float f = all > 0.f ? 1.f / all : 0.f;
-      reinterpret_cast<uint32_t*>(p.out + (static_cast<long long>(rq.t0 + t) * p.Hq + head) * kHeadDim)[lane] =
-          pack_bf16x2(z.x * f, z.y * f);
-      if (lane == 0)
-        p.lse[static_cast<long long>(head) * p.T + rq.t0 + t] = all > 0.f ? (ref + __log2f(all)) * kLn2 : -INFINITY;
-    }
-    r0 += 8;
-  } while (r0 < min(kR, rq.n * p.G - row0));
-}
-
 }  // namespace sa

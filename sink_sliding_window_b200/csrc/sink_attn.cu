@@ -21,8 +21,7 @@
 #include "paged_plan.cuh"
 #include "paged_append.cuh"
 #include "paged_attn.cuh"
-#include "paged_rows.cuh"
-#include "paged_chunk.cuh"
+#include "paged_join.cuh"
 
 namespace sa {
 namespace {
@@ -859,10 +858,11 @@ bool make_map_paged_q(CUtensorMap* map, const sink_attn_paged_dims* d, const voi
 
 template <bool kF8>
 bool launch_chunks(ChunkParams& p, const sink_attn_paged_dims* d, const void* k_cache, const void* v_cache,
-                   const PagedSplit& split, dim3* join, cudaStream_t st) {
+                   const PagedSplit& split, unsigned* join, cudaStream_t st) {
   const ChunkBound bound = chunk_bound<kF8>(d, split, p.a.window);
   if (bound.units > (1 << 30)) return false;
   p.wave = kChunkPerSm<kF8> * kChunkSms;
+  p.tiles = kChunkTiles<kF8>;
   CUtensorMap tm_q, tm_k, tm_v;
   const int box = std::min(d->page_size, kHalfN);
   p.a.box_log2 = ilog2_exact(box);
@@ -883,7 +883,7 @@ bool launch_chunks(ChunkParams& p, const sink_attn_paged_dims* d, const void* k_
   const bool turns = bound.parts == 0 || d->total_tokens < static_cast<int64_t>(d->batch) * d->max_new / 2;
   const int64_t places = bound.units + bound.parts;
   const unsigned ctas = static_cast<unsigned>(std::min<int64_t>(places, (turns ? 1 : kChunkMaxWaves + 1) * p.wave));
-  if (bound.parts) *join = dim3(static_cast<unsigned>(std::min<int64_t>(bound.units, p.wave - 1)), kChunkTiles<kF8> * kBlockM / 32);
+  if (bound.parts) *join = static_cast<unsigned>(std::min<int64_t>(bound.units, p.wave - 1)) * (p.tiles * kBlockM / 32);
   return launch_early(sink_attn_paged_chunk_kernel<kF8>, dim3(ctas), kChunkThreads<kF8>, chunk_smem_bytes<kF8>(), st, tm_q,
                       tm_k, tm_v, p);
 }
@@ -942,8 +942,9 @@ sink_attn_status paged_attn_impl(const sink_attn_paged_dims* d, const void* q, c
   p.part_ml = reinterpret_cast<float2*>(base + ws.ml);
   p.part_o = reinterpret_cast<float*>(base + ws.o);
   cudaStream_t st_ = static_cast<cudaStream_t>(stream);
-  ChunkParams c;
-  dim3 chunk_join(0), rows_join(0);
+  ChunkParams c = {};
+  unsigned chunk_join = 0;  // CTAs of the join
+  dim3 rows_join(0, 0, 1);
   if (split.chunks) {
     c.a = p;
     c.tokens = kBlockM / p.G;
@@ -958,12 +959,17 @@ sink_attn_status paged_attn_impl(const sink_attn_paged_dims* d, const void* q, c
   if (split.rows && !(codes ? launch_rows<true>(split.kR, p, d, k_cache, v_cache, split.chunks, &rows_join, st_)
                             : launch_rows<false>(split.kR, p, d, k_cache, v_cache, split.chunks, &rows_join, st_)))
     return SINK_ATTN_ERR_CUDA;
-  if (chunk_join.x && !launch_early(codes ? sink_attn_paged_chunk_join_kernel<true> : sink_attn_paged_chunk_join_kernel<false>,
-                                    chunk_join, 256, 0, st_, c))
+  if (chunk_join) {
+    c.a = p;
+    const int workers = static_cast<int>(rows_join.x);
+    if (!launch_early(split.kR == 8 ? sink_attn_paged_join_both_kernel<8> : sink_attn_paged_join_both_kernel<16>,
+                      dim3(chunk_join + rows_join.x * rows_join.y), 256, 0, st_, c, static_cast<int>(chunk_join), workers))
+      return SINK_ATTN_ERR_CUDA;
+  } else if (rows_join.x &&
+             !launch_early(split.kR == 8 ? sink_attn_paged_join_kernel<8> : sink_attn_paged_join_kernel<16>, rows_join, 256,
+                           0, st_, p)) {
     return SINK_ATTN_ERR_CUDA;
-  if (rows_join.x && !launch_early(split.kR == 8 ? sink_attn_paged_join_kernel<8> : sink_attn_paged_join_kernel<16>,
-                                   rows_join, 256, 0, st_, p))
-    return SINK_ATTN_ERR_CUDA;
+  }
   return SINK_ATTN_OK;
 }
 
