@@ -336,13 +336,16 @@ int sink_attn_decode_launches(const sink_attn_decode_dims* dims, int window);
  *     block_table[b][p / page_size] at offset p mod page_size; its slot is
  *     page * page_size + offset (int32; num_pages * page_size < 2^31).
  *     Entries of pages that no query of a call can see are not read and may
- *     hold anything, -1 for example; slots that hold no visible token may hold
- *     any bits, NaN included.
+ *     hold anything, -1 for example; slots that hold no token which some new
+ *     token of the request sees may hold any bits, NaN included.  The others
+ *     hold finite numbers: an infinity or a NaN in one may reach the rows of the
+ *     same request that do not see it.
  *   - The new tokens of a step are packed: request b's are rows
  *     cu_seqlens[b] .. cu_seqlens[b+1] - 1 of q.  kv_lens[b] counts its tokens
  *     after the step, so its new token t has position
  *     kv_lens[b] - (cu_seqlens[b+1] - cu_seqlens[b]) + t.
- *   - page_size is a power of two from 16 to 1024.
+ *   - page_size is a power of two from 16 to 1024.  A cache's rows do not
+ *     overlap: the stride of a dimension of several elements is at least D.
  *   - What only the device can see (a page outside the pool, lengths that do
  *     not fit) never leads to an access out of range: it is recorded as a
  *     device error (0x202 the pool ran dry, 0x203 a page outside the pool,
@@ -379,7 +382,8 @@ int sink_attn_decode_launches(const sink_attn_decode_dims* dims, int window);
  *     be first_page; other overlaps are not allowed.  Where they are distinct,
  *     the call can be repeated and gives the same again.
  *
- * batch is at most 4096.  batch = 0 is a no-op. */
+ * batch is at most 4096, batch * max_pages * page_size at most 2^30.  batch = 0
+ * is a no-op. */
 typedef struct {
     int batch;      /* requests */
     int max_tokens; /* entries of slot_map */
@@ -440,9 +444,14 @@ size_t sink_attn_paged_workspace_size(const sink_attn_paged_dims* dims);
  * device), sinks [Hq] fp32.  Writes out [T][Hq][D] bf16 (dense) and lse
  * [Hq][T] fp32 of the rows before cu_seqlens[batch]; rows behind them are left
  * as they were.  A row that sees no key gets out = 0 and lse = its sink.
- * G = Hq / Hkv is any whole number up to 128.  `workspace`: caller-owned,
- * 256-byte aligned, of sink_attn_paged_workspace_size(dims) bytes; calls whose
- * execution may overlap need one each.  T = 0 or batch = 0 is a no-op. */
+ * G = Hq / Hkv is any whole number up to 128; batch is at most 4096, and batch *
+ * max_pages * page_size * Hkv at most 2^35.  q_stride >= Hq * D where T > 1.
+ * Requests of up to 64 / G tokens and longer ones go to different kernels, which
+ * run side by side; max_new tells which of them a call needs, so a decode step
+ * should say 1.  Nothing is read back to the host: the lengths may change
+ * between replays of a captured call.  `workspace`: caller-owned, 256-byte
+ * aligned, of sink_attn_paged_workspace_size(dims) bytes and any content; calls
+ * whose execution may overlap need one each.  T = 0 or batch = 0 is a no-op. */
 sink_attn_status sink_attn_paged_attn(const sink_attn_paged_dims* dims,
                                       const void* q, const void* k_cache, const void* v_cache,
                                       const int* block_table, const int* cu_seqlens, const int* kv_lens,
@@ -451,7 +460,9 @@ sink_attn_status sink_attn_paged_attn(const sink_attn_paged_dims* dims,
                                       void* workspace, size_t workspace_bytes, void* stream);
 
 /* The same over e4m3 codes: key = code * k_scale[g], value = code * v_scale[g]
- * (fp32 [Hkv], device, > 0). */
+ * (fp32 [Hkv], device, > 0).  Codes are widened to fp16, exactly; q is rounded to
+ * fp16 (exact from 2^-14 up to 65504, where it saturates), and so are the
+ * softmax weights. */
 sink_attn_status sink_attn_paged_attn_e4m3(const sink_attn_paged_dims* dims,
                                            const void* q, const void* k_cache, const void* v_cache,
                                            const int* block_table, const int* cu_seqlens, const int* kv_lens,
