@@ -49,6 +49,7 @@ constexpr int kChunkMaxWaves = 3;  // of parts
 constexpr int kChunkFixed = 8;     // a part's set-up, ends and join, in 64-key steps
 constexpr int kChunkLeast = 4;     // steps of a part
 constexpr int kChunkMostParts = 32;  // of a unit
+constexpr int kChunkMaxUnits = 1 << 24;  // of a call; sums of lengths that do not fit stop there
 constexpr int kChunkSlots = 4;
 constexpr int kChunkSlotKeys = 64;
 constexpr int kChunkSlotBytes = kChunkSlotKeys * kHeadDim;  // e4m3 codes of K or V
@@ -58,6 +59,7 @@ struct ChunkParams {
   int tokens;          // P: tokens of a query tile
   int wave;            // CTAs that run at once
   int tiles;           // kTiles
+  int max_units, max_cut, max_parts;  // what the host counted on: units, cut ones, parts of them
   float* part_o;       // [part][kTiles * 128 rows][64]
   float2* part_ml;     // [part][kTiles * 128] (m in log2 units, l)
   int4* part_unit;     // [cut unit] (request, unit within its head, head, parts)
@@ -134,7 +136,7 @@ __device__ __forceinline__ void chunk_scan(ChunkCtl<kF8>* cc, int units, float s
     if (lane >= o) upto += v;
     steps += __shfl_xor_sync(0xffffffffu, steps, o);
   }
-  if (lane == 31) cc->units[warp] = upto, cc->steps[warp] = steps;
+  if (lane == 31) cc->units[warp] = min(upto, kChunkMaxUnits), cc->steps[warp] = steps;
   __syncthreads();
   all_units = 0;
   all_steps = 0.f;
@@ -182,7 +184,7 @@ __global__ void __launch_bounds__(kChunkThreads<kF8>, kChunkPerSm<kF8>)
       if (blockIdx.x == 0) paged_check(p.a, b0 + i);
       const PagedRequest r = paged_request(p.a, b0 + i);
       const int n = chunk_units<kF8>(p, r) * p.a.Hkv;
-      units += n;
+      units = min(units + min(n, kChunkMaxUnits), kChunkMaxUnits);
       steps += static_cast<float>(n) * chunk_steps<kF8>(p, r);
     }
     int upto, total;
@@ -190,8 +192,12 @@ __global__ void __launch_bounds__(kChunkThreads<kF8>, kChunkPerSm<kF8>)
     chunk_scan<kF8>(ctl, units, steps, upto, total, all_steps);
     ctl->starts[threadIdx.x] = upto - units;
     if (threadIdx.x == 0) {
+      // More units than rows can make come from cu_seqlens that do not increase
+      // (paged_check has told): none is taken.
+      if (total > p.max_units) total = 0;
       const int full = total / p.wave * p.wave, rest = total - full;
-      const int parts = p.part_o && rest ? chunk_parts(rest, static_cast<int>(all_steps / total), p.wave) : 1;
+      int parts = p.part_o && rest ? chunk_parts(rest, static_cast<int>(all_steps / total), p.wave) : 1;
+      if (rest > p.max_cut || rest * parts > p.max_parts) parts = 1;
       if (blockIdx.x == 0 && p.part_units) *p.part_units = parts > 1 ? rest : 0;
       ctl->total = total;
       ctl->full = parts > 1 ? full : total;

@@ -684,6 +684,10 @@ sink_attn_status check_paged_attn(const sink_attn_paged_dims* d, bool codes) {
     return SINK_ATTN_ERR_UNSUPPORTED;
   if (d->total_tokens > 1 && d->q_stride < static_cast<long long>(d->num_q_heads) * kHeadDim) return SINK_ATTN_ERR_SHAPE;
   if (d->q_stride >= (1ll << 38)) return SINK_ATTN_ERR_UNSUPPORTED;
+  // Units of the chunk kernel, of at least one 128-row tile each (or the end of a request).
+  const int tile = kBlockM / (d->num_q_heads / d->num_kv_heads);
+  if ((d->total_tokens / tile + std::min(d->batch, d->total_tokens)) * static_cast<int64_t>(d->num_kv_heads) >= kChunkMaxUnits)
+    return SINK_ATTN_ERR_UNSUPPORTED;
   if (d->q_stride % 8) return SINK_ATTN_ERR_ALIGN;
   return SINK_ATTN_OK;
 }
@@ -860,7 +864,6 @@ template <bool kF8>
 bool launch_chunks(ChunkParams& p, const sink_attn_paged_dims* d, const void* k_cache, const void* v_cache,
                    const PagedSplit& split, unsigned* join, cudaStream_t st) {
   const ChunkBound bound = chunk_bound<kF8>(d, split, p.a.window);
-  if (bound.units > (1 << 30)) return false;
   p.wave = kChunkPerSm<kF8> * kChunkSms;
   p.tiles = kChunkTiles<kF8>;
   CUtensorMap tm_q, tm_k, tm_v;
@@ -872,6 +875,9 @@ bool launch_chunks(ChunkParams& p, const sink_attn_paged_dims* d, const void* k_
   static SmemAttrOnce smem_set;
   if (!smem_set.ensure(sink_attn_paged_chunk_kernel<kF8>, chunk_smem_bytes<kF8>())) return false;
   if (bound.parts == 0) p.part_o = nullptr;
+  p.max_units = static_cast<int>(bound.units);
+  p.max_cut = static_cast<int>(std::min<int64_t>(bound.units, p.wave - 1));
+  p.max_parts = static_cast<int>(bound.parts);
   // Units too short to be cut (a window): one wave of CTAs, each taking its
   // turns, which saves every unit the start of a CTA.  Longer ones: a CTA for
   // each as far as four waves go, which the SMs even out among themselves;
@@ -883,7 +889,7 @@ bool launch_chunks(ChunkParams& p, const sink_attn_paged_dims* d, const void* k_
   const bool turns = bound.parts == 0 || d->total_tokens < static_cast<int64_t>(d->batch) * d->max_new / 2;
   const int64_t places = bound.units + bound.parts;
   const unsigned ctas = static_cast<unsigned>(std::min<int64_t>(places, (turns ? 1 : kChunkMaxWaves + 1) * p.wave));
-  if (bound.parts) *join = static_cast<unsigned>(std::min<int64_t>(bound.units, p.wave - 1)) * (p.tiles * kBlockM / 32);
+  if (bound.parts) *join = static_cast<unsigned>(p.max_cut * (p.tiles * kBlockM / 32));
   return launch_early(sink_attn_paged_chunk_kernel<kF8>, dim3(ctas), kChunkThreads<kF8>, chunk_smem_bytes<kF8>(), st, tm_q,
                       tm_k, tm_v, p);
 }

@@ -155,6 +155,30 @@ def test_two_graphs_with_a_workspace_each():
 
 
 @pytest.mark.gpu
+@KINDS
+def test_rows_counted_twice_stay_inside(e4m3):
+    """cu_seqlens that go back and forth make far more units than T rows can:
+    recorded, and nothing outside of the call's tensors is written."""
+    p = Paged([4000] * 8, [8] * 8, 8, 1, 64, 0, e4m3, seed=11, pad_rows=5)
+    a = p.device()
+    n = 64
+    cu = torch.tensor([0, p.T] * (n // 2) + [0], dtype=torch.int32, device="cuda")
+    lens = torch.full((n,), 4000, dtype=torch.int32, device="cuda")
+    table = a["block_table"].repeat(n // 8, 1).contiguous()
+    d = ops.PagedDims(n, p.rows, p.rows, 8, 1, 64, 64, p.pages, p.max_pages, a["k_cache"].stride(0), a["k_cache"].stride(1),
+                      64, a["q"].stride(0))
+    need = ops.load().sink_attn_paged_workspace_size(ctypes.byref(d))
+    ws = torch.full((need + (8 << 20),), 0x5A, dtype=torch.uint8, device="cuda")
+    out = torch.full((p.rows + 64, 8, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    for order in (cu, cu.flip(0).contiguous()):
+        ops.paged_attn(a["q"], a["k_cache"], a["v_cache"], table, order, lens, a["sinks"], out=out[:p.rows],
+                       k_scale=a["k_scale"], v_scale=a["v_scale"], workspace=ws[:need])
+        torch.cuda.synchronize()
+        assert ops.device_error() == 0x205
+        assert (ws[need:] == 0x5A).all() and (out[p.rows:] == 7).all()
+
+
+@pytest.mark.gpu
 def test_empty_step_and_empty_batch():
     p = Paged([40, 3], [1, 1], 4, 1, 16, 0, seed=10)
     a = p.device()
@@ -170,7 +194,7 @@ def test_empty_step_and_empty_batch():
 @pytest.mark.parametrize("bad,code", [
     (dict(page_stride=0), 2), (dict(token_stride=56), 2), (dict(head_stride=0), 2), (dict(page_stride=1 << 38), 4),
     (dict(q_stride=0), 2), (dict(q_stride=504), 2), (dict(q_stride=1 << 38), 4), (dict(batch=4097), 4),
-    (dict(batch=4096, max_pages=1 << 20), 4),
+    (dict(batch=4096, max_pages=1 << 20), 4), (dict(total_tokens=1 << 29, max_new=1 << 29), 4),
 ])
 def test_attn_rejects_strides_and_batches(L, bad, code):
     d = dict(batch=2, total_tokens=4, max_new=2, num_q_heads=8, num_kv_heads=2, head_dim=64, page_size=16, num_pages=9,
