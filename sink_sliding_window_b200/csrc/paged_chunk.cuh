@@ -66,9 +66,21 @@ struct ChunkParams {
   int* part_units;     // cut units of this call
 };
 
+// One round's work: a unit, or a part of it.
+struct ChunkUnit {
+  int b;                  // request, -1: none
+  PagedRequest rq;
+  int g, group;           // key/value head, unit within the request's head
+  int part, parts, slot;  // parts > 1: `part` of them, `slot` of the call's
+  // Where the barriers' phases stand when it begins: key tiles that have been
+  // through the ring, parity of q_full, q_conv and o_full, and of s_full and
+  // p_full (bit w: tile w's).
+  int ring;
+  uint32_t q_parity, s_parity;
+};
+
 template <bool kF8>
 struct ChunkCtl {
-  // Barriers, q_full to o_full.
   uint64_t q_full;
   uint64_t q_conv;                 // e4m3: Q converted to fp16 in place (all softmax threads)
   uint64_t k_full[kFwdStages];     // e4m3: two arrivals, of the widening warps
@@ -79,11 +91,11 @@ struct ChunkCtl {
   uint64_t s_full[kChunkTiles<kF8>];
   uint64_t p_full[kChunkTiles<kF8>];
   uint64_t o_full;
+  ChunkUnit unit[2];                   // by the round's parity
   int units[kChunkThreads<kF8> / 32];  // sums per warp
   float steps[kChunkThreads<kF8> / 32];
   int starts[kChunkThreads<kF8>];      // units before each thread's requests
   int total, full, parts;              // units, those of full waves, parts of each of the others
-  int unit[2];                         // request, unit within it
   uint32_t tmem_base;
   int abort;
 };
@@ -104,6 +116,40 @@ template <bool kF8>
 __device__ __forceinline__ int chunk_steps(const ChunkParams& p, const PagedRequest& r) {
   const int keys = max(r.len - r.n / 2, 1);
   return (p.a.window > 0 ? min(keys, p.a.window + kChunkTiles<kF8> * p.tokens) : keys) / kHalfN + 1;
+}
+
+// A unit's (or part's) first token within the request, keys, 128-key tiles and
+// 64-key steps.
+struct ChunkKeys {
+  int i0;
+  int key0, key_hi;  // first key of the first tile, last key that any row sees
+  int n_tiles, n_half;
+};
+
+template <bool kF8>
+__device__ __forceinline__ ChunkKeys chunk_keys(const ChunkParams& p, const ChunkUnit& u) {
+  ChunkKeys k;
+  const int tokens = kChunkTiles<kF8> * p.tokens, base = u.rq.len - u.rq.n;
+  k.i0 = u.group * tokens;
+  k.key_hi = base + min(k.i0 + tokens, u.rq.n) - 1;
+  const int lo = p.a.window > 0 ? max(0, base + k.i0 - p.a.window + 1) >> p.a.box_log2 << p.a.box_log2 : 0;
+  const int halves = k.key_hi < lo ? 1 : (k.key_hi - lo) / kHalfN + 1;
+  const int tiles = (halves + 1) / 2;
+  int tile0 = 0;
+  k.n_tiles = tiles;
+  if (u.parts > 1) {
+    tile0 = static_cast<int>(static_cast<int64_t>(tiles) * u.part / u.parts);
+    k.n_tiles = static_cast<int>(static_cast<int64_t>(tiles) * (u.part + 1) / u.parts) - tile0;
+  }
+  k.n_half = min(halves - 2 * tile0, 2 * k.n_tiles);
+  k.key0 = lo + tile0 * kBlockN;
+  return k;
+}
+
+// Query tiles of a unit that hold tokens: the last one of a request may have fewer.
+template <bool kF8>
+__device__ __forceinline__ int chunk_live(const ChunkParams& p, const ChunkUnit& u, const ChunkKeys& k) {
+  return min(kChunkTiles<kF8>, (u.rq.n - k.i0 + p.tokens - 1) / p.tokens);
 }
 
 // Parts of each of the `rest` units behind the last full wave, of about
@@ -210,85 +256,95 @@ __global__ void __launch_bounds__(kChunkThreads<kF8>, kChunkPerSm<kF8>)
   if (static_cast<int>(blockIdx.x) >= places) return;
 
   // A CTA takes one of every gridDim.x places in the list of units and parts,
-  // to and fro, since the units of a request get shorter along it.  (The first
-  // round's places all exist: CTAs without one have left.)
-  for (int round = 0;; ++round) {
+  // to and fro, since the units of a request get shorter along it.  The copying
+  // warp finds the next round's unit and looks up its first pages while the
+  // others compute (a window's unit takes 8 us, and this took 3 more when it
+  // came between two rounds); the barriers' phases run on from round to round.
+  int ring = 0;
+  uint32_t q_parity = 0, s_parity = 0;
+  auto prepare = [&](int round) -> int {  // by the whole warp; the lane's table entry of the first key tile
     const int first = round * static_cast<int>(gridDim.x);
-    if (first >= places) break;
     const int place = first + static_cast<int>(round & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-    if (place >= places) continue;
-    int unit = place, part = 0, parts = 1, slot = 0;
+    ChunkUnit u;
+    u.b = -1;
+    if (first >= places || place >= places) {  // nor is there one in any later round
+      if (lane == 0) ctl->unit[round & 1].b = -1;
+      return 0;
+    }
+    int unit = place;
+    u.part = u.slot = 0;
+    u.parts = 1;
     if (place >= ctl->full) {
-      parts = ctl->parts;
-      slot = place - ctl->full;
-      unit = ctl->full + slot / parts;
-      part = slot % parts;
+      u.parts = ctl->parts;
+      u.slot = place - ctl->full;
+      unit = ctl->full + u.slot / u.parts;
+      u.part = u.slot % u.parts;
     }
-    {
-      int at = ctl->starts[threadIdx.x];
-      if (unit >= at && unit < (threadIdx.x + 1 < kThreads ? ctl->starts[threadIdx.x + 1] : ctl->total)) {
-        for (int i = 0;; ++i) {
-          const int n = chunk_units<kF8>(p, paged_request(p.a, b0 + i)) * p.a.Hkv;
-          if (unit < at + n) {
-            ctl->unit[0] = b0 + i;
-            ctl->unit[1] = unit - at;
-            break;
-          }
-          at += n;
-        }
-      }
-      if (threadIdx.x == 0) {
-        // Fresh barriers each round; everything that arrived on those of the
-        // round before has been waited for.
-        if (round > 0) {
-          for (uint64_t* bar = &ctl->q_full; bar <= &ctl->o_full; ++bar)
-            asm volatile("mbarrier.inval.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
-        }
-        mbar_init(&ctl->q_full, 1);
-        mbar_init(&ctl->q_conv, kTiles * kBlockM);  // every softmax thread, with or without rows
-        for (int s = 0; s < kFwdStages; ++s) {
-          mbar_init(&ctl->k_full[s], kF8 ? 2 : 1);
-          mbar_init(&ctl->v_full[s], kF8 ? 2 : 1);
-          mbar_init(&ctl->kv_empty[s], 1);
-        }
-        for (int s = 0; s < kChunkSlots; ++s) {
-          mbar_init(&ctl->codes_full[s], 1);
-          mbar_init(&ctl->codes_empty[s], 1);
-        }
-        for (int w = 0; w < kTiles; ++w) {
-          mbar_init(&ctl->s_full[w], 1);
-          mbar_init(&ctl->p_full[w], kBlockM);
-        }
-        mbar_init(&ctl->o_full, 1);
-        fence_mbar_init();
-      }
-      if (round == 0 && warp == kMmaWarp) {
-        tmem_alloc(&ctl->tmem_base, 2 * kTmemO);
-        tmem_relinquish();
-      }
-      tc_fence_before();
-      __syncthreads();
-      tc_fence_after();
+    int thread = -1;  // the last one whose requests begin at or before the unit
+    for (int t = 0; t < kThreads; t += 32) thread += __popc(__ballot_sync(0xffffffffu, ctl->starts[t + lane] <= unit));
+    int at = ctl->starts[thread];
+    for (u.b = thread * per;; ++u.b) {
+      u.rq = paged_request(p.a, u.b);
+      const int n = chunk_units<kF8>(p, u.rq) * p.a.Hkv;
+      if (unit < at + n) break;
+      at += n;
     }
-    const uint32_t tmem = ctl->tmem_base;
-    const int b = ctl->unit[0];
-    const PagedRequest rq = paged_request(p.a, b);
-    const int g = ctl->unit[1] % p.a.Hkv;
-    const int group = chunk_units<kF8>(p, rq) - 1 - ctl->unit[1] / p.a.Hkv;
+    u.g = (unit - at) % p.a.Hkv;
+    u.group = chunk_units<kF8>(p, u.rq) - 1 - (unit - at) / p.a.Hkv;
+    u.ring = ring;
+    u.q_parity = q_parity;
+    u.s_parity = s_parity;
+    if (lane == 0) ctl->unit[round & 1] = u;
+    const ChunkKeys k = chunk_keys<kF8>(p, u);
+    ring += k.n_tiles;
+    if (k.n_half > 0) q_parity ^= 1;
+    if (k.n_half & 1) s_parity ^= (1u << chunk_live<kF8>(p, u, k)) - 1;
+    const int key = k.key0 + (lane << p.a.box_log2);
+    return lane < (kBlockN >> p.a.box_log2) && key <= k.key_hi ? paged_entry(p.a, u.b, key) : 0;
+  };
+  int first_entry = 0;
+  if (warp == kCopyWarp) first_entry = prepare(0);
+  if (threadIdx.x == 0) {
+    mbar_init(&ctl->q_full, 1);
+    mbar_init(&ctl->q_conv, kTiles * kBlockM);  // every softmax thread, with or without rows
+    for (int s = 0; s < kFwdStages; ++s) {
+      mbar_init(&ctl->k_full[s], kF8 ? 2 : 1);
+      mbar_init(&ctl->v_full[s], kF8 ? 2 : 1);
+      mbar_init(&ctl->kv_empty[s], 1);
+    }
+    for (int s = 0; s < kChunkSlots; ++s) {
+      mbar_init(&ctl->codes_full[s], 1);
+      mbar_init(&ctl->codes_empty[s], 1);
+    }
+    for (int w = 0; w < kTiles; ++w) {
+      mbar_init(&ctl->s_full[w], 1);
+      mbar_init(&ctl->p_full[w], kBlockM);
+    }
+    mbar_init(&ctl->o_full, 1);
+    fence_mbar_init();
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(&ctl->tmem_base, 2 * kTmemO);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ctl->tmem_base;
+
+  for (int round = 0;; ++round) {
+    const ChunkUnit& u = ctl->unit[round & 1];
+    const int b = u.b;
+    if (b < 0) break;
+    const PagedRequest rq = u.rq;
+    const int g = u.g;
     const int G = p.a.G, base = rq.len - rq.n;  // position of the request's first new token
-    const int i0 = group * kTiles * p.tokens;   // the unit's first token within the request
-    const int key_hi = base + min(i0 + kTiles * p.tokens, rq.n) - 1;  // the last key any row sees
+    const ChunkKeys keys = chunk_keys<kF8>(p, u);
+    const int i0 = keys.i0, key_hi = keys.key_hi, key0 = keys.key0, n_tiles = keys.n_tiles, n_half = keys.n_half;
     const int box_log2 = p.a.box_log2;
-    const int key_lo = p.a.window > 0 ? max(0, base + i0 - p.a.window + 1) >> box_log2 << box_log2 : 0;
-    // This part's 128-key tiles and 64-key steps.
-    const int halves = key_hi < key_lo ? 1 : (key_hi - key_lo) / kHalfN + 1;
-    const int tiles = (halves + 1) / 2;
-    const int tile0 = static_cast<int>(static_cast<int64_t>(tiles) * part / parts);
-    const int n_tiles = static_cast<int>(static_cast<int64_t>(tiles) * (part + 1) / parts) - tile0;
-    const int n_half = min(halves - 2 * tile0, 2 * n_tiles);
-    const int key0 = key_lo + tile0 * kBlockN;
-    // Tiles that hold tokens: the last unit of a request may have fewer than kTiles.
-    const int live = min(kTiles, (rq.n - i0 + p.tokens - 1) / p.tokens);
+    const int live = chunk_live<kF8>(p, u, keys);
+    const int ring0 = u.ring;  // tile j of the unit is the ring's ring0 + j
+    const uint32_t qp = u.q_parity, sp = u.s_parity;
 
     if (warp >= kMmaWarp) {
       if (warp == kMmaWarp) {
@@ -297,29 +353,30 @@ __global__ void __launch_bounds__(kChunkThreads<kF8>, kChunkPerSm<kF8>)
         // S_b(h+1) into the buffer that P_b(h) just left.
         if (n_half > 0 && elect_one()) {
           mbar_arrive_expect_tx(&ctl->q_full, kTiles * p.tokens * G * kHeadDim * 2);
-          for (int u = 0; u < kTiles; ++u)
-            tma_load_3d(sQ + u * kTileBytes, &tm_q, &ctl->q_full, 0, g * G, rq.t0 + i0 + u * p.tokens);
+          for (int w = 0; w < kTiles; ++w)
+            tma_load_3d(sQ + w * kTileBytes, &tm_q, &ctl->q_full, 0, g * G, rq.t0 + i0 + w * p.tokens);
           const uint32_t tS = tmem;
           const uint32_t tO = tmem + kTmemO;
-          bool ok = mbar_wait(kF8 ? &ctl->q_conv : &ctl->q_full, 0, abort, &g_device_error, kDevErrTimeoutMma) &&
-                    mbar_wait(&ctl->k_full[0], 0, abort, &g_device_error, kDevErrTimeoutMma);
+          const int s0 = ring0 % kFwdStages;
+          bool ok = mbar_wait(kF8 ? &ctl->q_conv : &ctl->q_full, qp, abort, &g_device_error, kDevErrTimeoutMma) &&
+                    mbar_wait(&ctl->k_full[s0], (ring0 / kFwdStages) & 1, abort, &g_device_error, kDevErrTimeoutMma);
           if (ok) {
             tc_fence_after();
 #pragma unroll
             for (int w = 0; w < kTiles; ++w) {
               if (w >= live) break;
-              fwd_issue_qk<kF8>(tS + w * kHalfN, smem_u32(sQ + w * kTileBytes), smem_u32(sK));
+              fwd_issue_qk<kF8>(tS + w * kHalfN, smem_u32(sQ + w * kTileBytes), smem_u32(sK + s0 * kTileBytes));
               tc_commit(&ctl->s_full[w]);
             }
           }
           for (int h = 0; ok && h < n_half; ++h) {
-            const int j = h >> 1, s = j % kFwdStages;
-            const int hn = h + 1, jn = hn >> 1, sn = jn % kFwdStages;
+            const int j = ring0 + (h >> 1), s = j % kFwdStages;
+            const int hn = h + 1, jn = ring0 + (hn >> 1), sn = jn % kFwdStages;
             ok = mbar_wait(&ctl->v_full[s], (j / kFwdStages) & 1, abort, &g_device_error, kDevErrTimeoutMma) &&
                  (hn >= n_half ||
                   mbar_wait(&ctl->k_full[sn], (jn / kFwdStages) & 1, abort, &g_device_error, kDevErrTimeoutMma));
             for (int w = 0; ok && w < live; ++w) {
-              ok = mbar_wait(&ctl->p_full[w], h & 1, abort, &g_device_error, kDevErrTimeoutMma);
+              ok = mbar_wait(&ctl->p_full[w], (h ^ (sp >> w)) & 1, abort, &g_device_error, kDevErrTimeoutMma);
               if (!ok) break;
               tc_fence_after();
               fwd_issue_pv<kF8>(tO + w * kHeadDim, tS + w * kHalfN, smem_u32(sV + s * kTileBytes) + (h & 1) * kHalfBytes,
@@ -332,13 +389,7 @@ __global__ void __launch_bounds__(kChunkThreads<kF8>, kChunkPerSm<kF8>)
             }
             if (ok && ((h & 1) == 1 || h == n_half - 1)) tc_commit(&ctl->kv_empty[s]);
           }
-          if (ok) {
-            tc_commit(&ctl->o_full);
-            // The commits that nobody else waits for, before the next round's
-            // barriers take their place.
-            for (int j = max(0, n_tiles - kFwdStages); j < n_tiles; ++j)
-              mbar_wait(&ctl->kv_empty[j % kFwdStages], (j / kFwdStages) & 1, abort, &g_device_error, kDevErrTimeoutMma);
-          }
+          if (ok) tc_commit(&ctl->o_full);
         }
       } else if (!kF8 && warp == kCopyWarp) {
         // ---------------------------------------------------------- TMA producer
@@ -346,15 +397,14 @@ __global__ void __launch_bounds__(kChunkThreads<kF8>, kChunkPerSm<kF8>)
         const int nbox = kBlockN >> box_log2, page_mask = (1 << p.a.page_log2) - 1;
         auto wanted = [&](int j) { return lane < nbox && key0 + j * kBlockN + (lane << box_log2) <= key_hi; };
         auto entry = [&](int j) { return paged_entry(p.a, b, key0 + j * kBlockN + (lane << box_log2)); };
-        int next = wanted(0) ? entry(0) : 0;
+        int next = first_entry;
         bool ok = true;
         for (int j = 0; ok && j < n_tiles; ++j) {
-          const int s = j % kFwdStages;
+          const int s = (ring0 + j) % kFwdStages, turn = (ring0 + j) / kFwdStages;
           const int mine = wanted(j) ? paged_page(p.a, next) : p.a.num_pages;
           if (j + 1 < n_tiles && wanted(j + 1)) next = entry(j + 1);
-          if (j >= kFwdStages)
-            ok = warp_all(mbar_wait(&ctl->kv_empty[s], ((j / kFwdStages) - 1) & 1, abort, &g_device_error,
-                                    kDevErrTimeoutProducer));
+          if (turn > 0)
+            ok = warp_all(mbar_wait(&ctl->kv_empty[s], (turn - 1) & 1, abort, &g_device_error, kDevErrTimeoutProducer));
           if (!ok) break;
           if (elect_one()) {
             mbar_arrive_expect_tx(&ctl->k_full[s], kTileBytes);
@@ -369,6 +419,7 @@ __global__ void __launch_bounds__(kChunkThreads<kF8>, kChunkPerSm<kF8>)
           }
           __syncwarp();
         }
+        first_entry = prepare(round + 1);
       } else if (kF8 && warp == kCopyWarp) {
         // ------------------------------------------------------ e4m3: TMA producer
         // Slot q holds 64 keys: of tile q / 4 those of K, two slots, then those of V.
@@ -376,7 +427,7 @@ __global__ void __launch_bounds__(kChunkThreads<kF8>, kChunkPerSm<kF8>)
         const int per_slot = kChunkSlotKeys >> box_log2;
         auto wanted = [&](int j) { return lane < nbox && key0 + j * kBlockN + (lane << box_log2) <= key_hi; };
         auto entry = [&](int j) { return paged_entry(p.a, b, key0 + j * kBlockN + (lane << box_log2)); };
-        int next = wanted(0) ? entry(0) : 0, mine = 0;
+        int next = first_entry, mine = 0;
         bool ok = true;
         for (int q = 0; ok && q < 4 * n_tiles; ++q) {
           const int j = q >> 2, e = q & 3, at_slot = q % kChunkSlots;
@@ -384,8 +435,8 @@ __global__ void __launch_bounds__(kChunkThreads<kF8>, kChunkPerSm<kF8>)
             mine = wanted(j) ? paged_page(p.a, next) : p.a.num_pages;
             if (j + 1 < n_tiles && wanted(j + 1)) next = entry(j + 1);
           }
-          if (q >= kChunkSlots)
-            ok = warp_all(mbar_wait(&ctl->codes_empty[at_slot], ((q / kChunkSlots) - 1) & 1, abort, &g_device_error,
+          if (ring0 + j > 0)  // (four slots: each holds one of a tile's four)
+            ok = warp_all(mbar_wait(&ctl->codes_empty[at_slot], (ring0 + j - 1) & 1, abort, &g_device_error,
                                     kDevErrTimeoutProducer));
           if (!ok) break;
           uint64_t* full = &ctl->codes_full[at_slot];
@@ -399,17 +450,18 @@ __global__ void __launch_bounds__(kChunkThreads<kF8>, kChunkPerSm<kF8>)
           }
           __syncwarp();
         }
+        first_entry = prepare(round + 1);
       } else if (kF8) {
         // ------------------------------------------------------------ e4m3: widen
         // This warp takes every other slot.  Rows that no row of the request sees
         // become zeros.
         bool ok = true;
         for (int q = warp - kCopyWarp - 1; q < 4 * n_tiles; q += 2) {
-          const int j = q >> 2, e = q & 3, s = j % kFwdStages, at_slot = q % kChunkSlots;
-          if (e < 2 && j >= kFwdStages)
-            ok = warp_all(mbar_wait(&ctl->kv_empty[s], ((j / kFwdStages) - 1) & 1, abort, &g_device_error,
-                                    kDevErrTimeoutProducer));
-          ok = ok && warp_all(mbar_wait(&ctl->codes_full[at_slot], (q / kChunkSlots) & 1, abort, &g_device_error,
+          const int j = q >> 2, e = q & 3, at_slot = q % kChunkSlots;
+          const int s = (ring0 + j) % kFwdStages, turn = (ring0 + j) / kFwdStages;
+          if (e < 2 && turn > 0)
+            ok = warp_all(mbar_wait(&ctl->kv_empty[s], (turn - 1) & 1, abort, &g_device_error, kDevErrTimeoutProducer));
+          ok = ok && warp_all(mbar_wait(&ctl->codes_full[at_slot], (ring0 + j) & 1, abort, &g_device_error,
                                         kDevErrTimeoutProducer));
           if (!ok) break;
           uint4 v[8];
@@ -442,6 +494,8 @@ __global__ void __launch_bounds__(kChunkThreads<kF8>, kChunkPerSm<kF8>)
       }
     } else {
       // --------------------------------------------- softmax (1 row per thread)
+      // (What the steps' loop does not need often is read from `u` again: it has
+      // no register to spare.)
       const int wg = warp >> 2;
       const int r = threadIdx.x & (kBlockM - 1);
       const int row_t = r / G;
@@ -465,7 +519,7 @@ __global__ void __launch_bounds__(kChunkThreads<kF8>, kChunkPerSm<kF8>)
       const float s2 = valid ? *(p.a.sinks + h) * kLog2e : 0.f;
       if constexpr (kF8) {
         if (n_half > 0 && wg >= live) mbar_arrive(&ctl->q_conv);
-        ok = ok && warp_all(mbar_wait(&ctl->q_full, 0, abort, &g_device_error, kDevErrTimeoutSoftmax));
+        ok = ok && warp_all(mbar_wait(&ctl->q_full, qp, abort, &g_device_error, kDevErrTimeoutSoftmax));
         if (ok) {
           // Rows of 128 bytes, so elementwise in place whatever the swizzle.
           uint32_t* row = reinterpret_cast<uint32_t*>(sQ + wg * kTileBytes + r * 128);
@@ -480,7 +534,7 @@ __global__ void __launch_bounds__(kChunkThreads<kF8>, kChunkPerSm<kF8>)
       }
 
       for (int hs = 0; ok && hs < n_half; ++hs) {
-        ok = warp_all(mbar_wait(&ctl->s_full[wg], hs & 1, abort, &g_device_error, kDevErrTimeoutSoftmax));
+        ok = warp_all(mbar_wait(&ctl->s_full[wg], (hs ^ (u.s_parity >> wg)) & 1, abort, &g_device_error, kDevErrTimeoutSoftmax));
         if (!ok) break;
         tc_fence_after();
         uint32_t sr[kHalfN];
@@ -509,12 +563,12 @@ __global__ void __launch_bounds__(kChunkThreads<kF8>, kChunkPerSm<kF8>)
         if constexpr (!kF8) {
           // Keys of the step that no row of the request sees: zero rows of V.
           // Both warpgroups write them, each before its own PV.
-          if (ks < rq.lo || ks + kHalfN > rq.len) {
-            const int j = hs >> 1, s = j % kFwdStages;
+          if (ks < u.rq.lo || ks + kHalfN > u.rq.len) {
+            const int j = u.ring + (hs >> 1), s = j % kFwdStages;
             ok = warp_all(mbar_wait(&ctl->v_full[s], (j / kFwdStages) & 1, abort, &g_device_error, kDevErrTimeoutSoftmax));
             if (!ok) break;
             const int key = ks + (r >> 1);
-            if (key < rq.lo || key >= rq.len) {
+            if (key < u.rq.lo || key >= u.rq.len) {
               uint4* row = reinterpret_cast<uint4*>(sV + s * kTileBytes + ((hs & 1) * kHalfN + (r >> 1)) * 128 + (r & 1) * 64);
 #pragma unroll
               for (int c = 0; c < 4; ++c) row[c] = make_uint4(0u, 0u, 0u, 0u);
@@ -528,29 +582,31 @@ __global__ void __launch_bounds__(kChunkThreads<kF8>, kChunkPerSm<kF8>)
 
       // ---------------------------------------------------------------- epilogue
       if (n_half == 0) {
-        p.part_ml[static_cast<long long>(slot) * kTiles * kBlockM + wg * kBlockM + r] = make_float2(-INFINITY, 0.f);
-        if (part == 0 && threadIdx.x == 0) p.part_unit[slot / parts] = make_int4(b, group, g, parts);
+        p.part_ml[static_cast<long long>(u.slot) * kTiles * kBlockM + wg * kBlockM + r] = make_float2(-INFINITY, 0.f);
+        if (u.part == 0 && threadIdx.x == 0) p.part_unit[u.slot / u.parts] = make_int4(u.b, u.group, u.g, u.parts);
       }
-      if (ok) ok = mbar_wait(&ctl->o_full, 0, abort, &g_device_error, kDevErrTimeoutEpilogue);
+      if (ok) ok = mbar_wait(&ctl->o_full, u.q_parity, abort, &g_device_error, kDevErrTimeoutEpilogue);
       ok = warp_all(ok);
       if (ok) {
         tc_fence_after();
         uint32_t o[kHeadDim];
         __syncwarp();
         tmem_ld64(tO, o);
-        const float vs = kF8 ? *(p.a.v_scale + g) : 1.f;
-        if (parts > 1) {
-          const long long at = static_cast<long long>(slot) * kTiles * kBlockM + wg * kBlockM + r;
+        const float vs = kF8 ? *(p.a.v_scale + u.g) : 1.f;
+        const int row_e = r / G, it_e = (u.group * kTiles + wg) * p.tokens + row_e, h_e = u.g * G + r - row_e * G;
+        const bool valid_e = row_e < p.tokens && it_e < u.rq.n;
+        if (u.parts > 1) {
+          const long long at = static_cast<long long>(u.slot) * kTiles * kBlockM + wg * kBlockM + r;
           p.part_ml[at] = make_float2(m_ref, l);
-          if (part == 0 && threadIdx.x == 0) p.part_unit[slot / parts] = make_int4(b, group, g, parts);
+          if (u.part == 0 && threadIdx.x == 0) p.part_unit[u.slot / u.parts] = make_int4(u.b, u.group, u.g, u.parts);
           float4* dst = reinterpret_cast<float4*>(p.part_o + at * kHeadDim);
-          if (valid) {
+          if (valid_e) {
 #pragma unroll
             for (int c = 0; c < kHeadDim / 4; ++c)
               dst[c] = make_float4(__uint_as_float(o[4 * c]) * vs, __uint_as_float(o[4 * c + 1]) * vs,
                                    __uint_as_float(o[4 * c + 2]) * vs, __uint_as_float(o[4 * c + 3]) * vs);
           }
-        } else if (valid) {
+        } else {
           const float top = fmaxf(s2, m_ref);
           float f = 0.f, all = 0.f;
           if (top != -INFINITY) {
@@ -558,8 +614,12 @@ __global__ void __launch_bounds__(kChunkThreads<kF8>, kChunkPerSm<kF8>)
             all = fmaf(l, f, s2 == top ? 1.f : ex2_approx(s2 - top));
           }
           f = all > 0.f ? vs * f / all : 0.f;
-          const int t = rq.t0 + it;
-          uint4* dst = reinterpret_cast<uint4*>(p.a.out + (static_cast<long long>(t) * p.a.Hq + h) * kHeadDim);
+          const int t = u.rq.t0 + it_e;
+          if (valid_e) p.a.lse[static_cast<long long>(h_e) * p.a.T + t] = all > 0.f ? (top + __log2f(all)) * kLn2 : -INFINITY;
+          // The warp's 32 rows through its part of the Q tile, which no MMA reads
+          // any more, so that eight lanes write a row's 128 bytes (rows written
+          // each by its own thread took 1.9 us).
+          uint8_t* rows = sQ + wg * kTileBytes + (r & ~31) * 128;
 #pragma unroll
           for (int c = 0; c < kHeadDim / 8; ++c) {
             uint4 v;
@@ -567,13 +627,23 @@ __global__ void __launch_bounds__(kChunkThreads<kF8>, kChunkPerSm<kF8>)
             v.y = pack_bf16x2(__uint_as_float(o[8 * c + 2]) * f, __uint_as_float(o[8 * c + 3]) * f);
             v.z = pack_bf16x2(__uint_as_float(o[8 * c + 4]) * f, __uint_as_float(o[8 * c + 5]) * f);
             v.w = pack_bf16x2(__uint_as_float(o[8 * c + 6]) * f, __uint_as_float(o[8 * c + 7]) * f);
-            dst[c] = v;
+            *reinterpret_cast<uint4*>(rows + lane * 128 + ((c ^ (lane & 7)) << 4)) = v;
           }
-          p.a.lse[static_cast<long long>(h) * p.a.T + t] = all > 0.f ? (top + __log2f(all)) * kLn2 : -INFINITY;
+          const long long mine = valid_e ? (static_cast<long long>(t) * p.a.Hq + h_e) * kHeadDim : -1;
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int row = 4 * i + (lane >> 3), c = lane & 7;
+            const uint4 v = *reinterpret_cast<const uint4*>(rows + row * 128 + ((c ^ (row & 7)) << 4));
+            const long long to = __shfl_sync(0xffffffffu, mine, row);
+            if (to >= 0) *reinterpret_cast<uint4*>(p.a.out + to + 8 * c) = v;
+          }
+          fence_proxy_async_smem();  // before the next round's Q
         }
       }
     }
 
+    __syncwarp();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();

@@ -4,7 +4,7 @@ chunks over bf16 and e4m3 pages), run under random interleavings (CPU only).
 The same model of barriers, tensor-core queue and TMA completions as the other
 kernels' (test_barrier_protocols.py).  Besides phases and deadlocks it checks
 that no copy or widening writes a buffer that is still read, and that nothing
-is in flight when a chunk CTA sets up the next round's barriers.  The models
+is in flight when a chunk CTA goes on to its next round.  The models
 follow the kernels' barrier use and are kept in step with them by hand."""
 import random
 
@@ -83,11 +83,24 @@ def test_rows_protocol(counts, stages):
 
 
 # ----------------------------------------------------------------- chunks
-def chunk_model(codes, tiles, live, n_half, rng):
-    """One round of a chunk CTA: n_half 64-key steps, `live` of its `tiles`
-    query tiles hold tokens; codes: e4m3, with a copying and two widening warps."""
-    n_tiles = (n_half + 1) // 2
+def chunk_model(codes, tiles, rounds, rng):
+    """A chunk CTA over several rounds (n_half 64-key steps, `live` of its `tiles`
+    query tiles hold tokens); codes: e4m3, with a copying and two widening
+    warps.  The barriers' phases run on from round to round."""
     bars = {}
+    state = dict(bars=bars, ring=0, q=0, s=[0] * tiles)
+    for n_half, live in rounds:
+        _chunk_round(codes, tiles, live, n_half, rng, state)
+
+
+def _chunk_round(codes, tiles, live, n_half, rng, state):
+    n_tiles = (n_half + 1) // 2
+    bars, ring, q0, s0 = state["bars"], state["ring"], state["q"], list(state["s"])
+    # What the copying warp works out for the round: the ring's place and parities.
+    state["ring"] += n_tiles
+    state["q"] += n_half > 0
+    for w in range(live):
+        state["s"][w] += n_half
 
     def bar(name, count=1):
         return bars.setdefault(name, Bar(name, count))
@@ -99,8 +112,9 @@ def chunk_model(codes, tiles, live, n_half, rng):
         bar(("codes_full", s)), bar(("codes_empty", s))
     for w in range(tiles):
         bar(("s_full", w)), bar(("p_full", w))
-    k_buf, v_buf, c_buf = ([Buffer((n, s)) for s in range(k)] for n, k in (("K", 2), ("V", 2), ("codes", 4)))
-    s_tmem = [Buffer(("S", w)) for w in range(tiles)]
+    if "buffers" not in state:
+        state["buffers"] = [[Buffer((n, s)) for s in range(k)] for n, k in (("K", 2), ("V", 2), ("codes", 4), ("S", tiles))]
+    k_buf, v_buf, c_buf, s_tmem = state["buffers"]
     tc, tma, ended = [], [], []
 
     def mma():
@@ -109,11 +123,11 @@ def chunk_model(codes, tiles, live, n_half, rng):
             return
         bar("q_full").arrive(expect_tx=tiles)
         tma.extend([lambda: bar("q_full").complete_tx(1)] * tiles)
-        yield from _wait(bar("q_conv") if codes else bar("q_full"), 0)
-        yield from _wait(bar(("k_full", 0)), 0)
+        yield from _wait(bar("q_conv") if codes else bar("q_full"), q0)
+        yield from _wait(bar(("k_full", ring % 2)), ring // 2)
 
         def qk(w, h):
-            j = h // 2
+            j = ring + h // 2
             k_buf[j % 2].begin(j)
 
             def run():
@@ -126,12 +140,13 @@ def chunk_model(codes, tiles, live, n_half, rng):
             qk(w, 0)
         yield "step"
         for h in range(n_half):
-            j, hn = h // 2, h + 1
+            j, hn = ring + h // 2, h + 1
+            jn = ring + hn // 2
             yield from _wait(bar(("v_full", j % 2)), j // 2)
             if hn < n_half:
-                yield from _wait(bar(("k_full", hn // 2 % 2)), hn // 2 // 2)
+                yield from _wait(bar(("k_full", jn % 2)), jn // 2)
             for w in range(live):
-                yield from _wait(bar(("p_full", w)), h)
+                yield from _wait(bar(("p_full", w)), s0[w] + h)
                 v_buf[j % 2].begin(j)
                 s_tmem[w].begin(("P", h))
 
@@ -145,12 +160,10 @@ def chunk_model(codes, tiles, live, n_half, rng):
             if h % 2 == 1 or h == n_half - 1:
                 tc.append(lambda j=j: bar(("kv_empty", j % 2)).arrive())
         tc.append(lambda: bar("o_full").arrive())
-        for j in range(max(0, n_tiles - 2), n_tiles):
-            yield from _wait(bar(("kv_empty", j % 2)), j // 2)
         ended.append("mma")
 
     def copy_tiles():
-        for j in range(n_tiles):
+        for j in range(ring, ring + n_tiles):
             s = j % 2
             if j >= 2:
                 yield from _wait(bar(("kv_empty", s)), j // 2 - 1)
@@ -162,7 +175,7 @@ def chunk_model(codes, tiles, live, n_half, rng):
         ended.append("copy")
 
     def copy_codes():
-        for q in range(4 * n_tiles):
+        for q in range(4 * ring, 4 * (ring + n_tiles)):
             s = q % 4
             if q >= 4:
                 yield from _wait(bar(("codes_empty", s)), q // 4 - 1)
@@ -173,7 +186,7 @@ def chunk_model(codes, tiles, live, n_half, rng):
         ended.append("copy")
 
     def widen(which):
-        for q in range(which, 4 * n_tiles, 2):
+        for q in range(4 * ring + which, 4 * (ring + n_tiles), 2):
             j, e = q // 4, q % 4
             s = j % 2
             if e < 2 and j >= 2:
@@ -195,27 +208,27 @@ def chunk_model(codes, tiles, live, n_half, rng):
             ended.append("softmax")
             return
         if codes:
-            yield from _wait(bar("q_full"), 0)
+            yield from _wait(bar("q_full"), q0)
             bar("q_conv").arrive()
         for h in range(n_half):
-            yield from _wait(bar(("s_full", w)), h)
+            yield from _wait(bar(("s_full", w)), s0[w] + h)
             s_tmem[w].begin(("S", h))
             yield from _steps(3, rng)
             s_tmem[w].end()
             s_tmem[w].write(("P", h))
             if rng.random() < 0.2:  # a step with keys that nobody sees: rows of V are zeroed
-                j = h // 2
+                j = ring + h // 2
                 yield from _wait(bar(("v_full", j % 2)), j // 2)
                 assert v_buf[j % 2].holds == j
             bar(("p_full", w)).arrive()
             yield "step"
-        yield from _wait(bar("o_full"), 0)
+        yield from _wait(bar("o_full"), q0)
         ended.append("softmax")
 
     agents = [mma()] + [softmax(w) for w in range(tiles)]
     agents += [copy_codes(), widen(0), widen(1)] if codes else [copy_tiles()]
 
-    def sync():  # the CTA's barrier at the end of a round: new barriers take the old ones' place
+    def sync():  # the CTA's barrier at the end of a round: Q and TMEM change hands
         while len(ended) < len(agents) - 1:
             yield "blocked"
         assert not tc and not tma, "in flight at the end of a round"
@@ -229,7 +242,14 @@ def chunk_model(codes, tiles, live, n_half, rng):
 def test_chunk_protocol(codes, tiles, n_half):
     for seed in range(12):
         rng = random.Random(seed)
-        chunk_model(codes, tiles, rng.randint(1, tiles), n_half, rng)
+        chunk_model(codes, tiles, [(n_half, rng.randint(1, tiles))], rng)
+
+
+@pytest.mark.parametrize("codes,tiles", [(False, 2), (True, 4)], ids=["bf16", "e4m3"])
+def test_chunk_protocol_over_rounds(codes, tiles):
+    for seed in range(30):
+        rng = random.Random(seed)
+        chunk_model(codes, tiles, [(rng.choice([0, 1, 2, 3, 3, 4, 5]), rng.randint(1, tiles)) for _ in range(7)], rng)
 
 
 def test_model_sees_a_stage_freed_too_early():

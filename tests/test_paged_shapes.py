@@ -45,9 +45,9 @@ def test_drawn_batches(seed):
 @KINDS
 @pytest.mark.parametrize("window", [0, 100])
 def test_more_units_than_ctas(e4m3, window):
-    """A unit of 8 (e4m3: 16) tokens and far more of them than CTAs run at
-    once: CTAs take several turns."""
-    p = Paged([600, 100, 350], [600, 100, 300], 64, 2, 32, window, e4m3, seed=1)
+    """A unit of 2 (e4m3: 4) tokens and far more of them than CTAs run at
+    once: CTAs take up to four turns."""
+    p = Paged([700, 100, 350, 611], [700, 100, 300, 33], 256, 2, 32, window, e4m3, seed=1)
     p.check(*p.run(ops))
 
 
