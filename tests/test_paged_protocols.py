@@ -3,8 +3,8 @@ chunks over bf16 and e4m3 pages), run under random interleavings (CPU only).
 
 The same model of barriers, tensor-core queue and TMA completions as the other
 kernels' (test_barrier_protocols.py).  Besides phases and deadlocks it checks
-that no copy or widening writes a buffer that is still read, and that nothing
-is in flight when a chunk CTA goes on to its next round.  The models
+that no copy or widening writes a buffer that is still read, and that no MMA is
+in flight when a chunk CTA goes on to its next round.  The models
 follow the kernels' barrier use and are kept in step with them by hand."""
 import random
 
@@ -88,13 +88,16 @@ def chunk_model(codes, tiles, rounds, rng):
     query tiles hold tokens); codes: e4m3, with a copying and two widening
     warps.  The barriers' phases run on from round to round."""
     bars = {}
-    state = dict(bars=bars, ring=0, q=0, s=[0] * tiles)
-    for n_half, live in rounds:
-        _chunk_round(codes, tiles, live, n_half, rng, state)
+    state = dict(bars=bars, ring=0, q=0, s=[0] * tiles, copied=0)
+    for i, (n_half, live) in enumerate(rounds):
+        following = (rounds[i + 1][0] + 1) // 2 if i + 1 < len(rounds) else 0
+        _chunk_round(codes, tiles, live, n_half, rng, state, following)
 
 
-def _chunk_round(codes, tiles, live, n_half, rng, state):
+def _chunk_round(codes, tiles, live, n_half, rng, state, following):
     n_tiles = (n_half + 1) // 2
+    # The copying warp is ahead: it ends the round with the next one's first tiles.
+    copy_to = state["ring"] + n_tiles + min(following, 1 if codes else 2)
     bars, ring, q0, s0 = state["bars"], state["ring"], state["q"], list(state["s"])
     # What the copying warp works out for the round: the ring's place and parities.
     state["ring"] += n_tiles
@@ -163,7 +166,7 @@ def _chunk_round(codes, tiles, live, n_half, rng, state):
         ended.append("mma")
 
     def copy_tiles():
-        for j in range(ring, ring + n_tiles):
+        for j in range(state["copied"], copy_to):
             s = j % 2
             if j >= 2:
                 yield from _wait(bar(("kv_empty", s)), j // 2 - 1)
@@ -175,7 +178,7 @@ def _chunk_round(codes, tiles, live, n_half, rng, state):
         ended.append("copy")
 
     def copy_codes():
-        for q in range(4 * ring, 4 * (ring + n_tiles)):
+        for q in range(4 * state["copied"], 4 * copy_to):
             s = q % 4
             if q >= 4:
                 yield from _wait(bar(("codes_empty", s)), q // 4 - 1)
@@ -231,10 +234,11 @@ def _chunk_round(codes, tiles, live, n_half, rng, state):
     def sync():  # the CTA's barrier at the end of a round: Q and TMEM change hands
         while len(ended) < len(agents) - 1:
             yield "blocked"
-        assert not tc and not tma, "in flight at the end of a round"
+        assert not tc, "in flight at the end of a round"
 
     agents.append(sync())
     _run(agents, tc, tma, rng)
+    state["copied"] = copy_to
 
 
 @pytest.mark.parametrize("codes,tiles", [(False, 2), (True, 4)], ids=["bf16", "e4m3"])
