@@ -417,8 +417,7 @@ __global__ void __launch_bounds__(kChunkThreads<kF8>, kChunkPerSm<kF8>)
       const int g = u.g;
       const int G = p.a.G, base = rq.len - rq.n;  // position of the request's first new token
       const ChunkKeys keys = chunk_keys<kF8>(p, u);
-      const int i0 = keys.i0, key_hi = keys.key_hi, key0 = keys.key0, n_tiles = keys.n_tiles, n_half = keys.n_half;
-      const int box_log2 = p.a.box_log2;
+      const int i0 = keys.i0, key0 = keys.key0, n_tiles = keys.n_tiles, n_half = keys.n_half;
       const int live = chunk_live<kF8>(p, u, keys);
       const int ring0 = u.ring;  // tile j of the unit is the ring's ring0 + j
       const uint32_t qp = u.q_parity, sp = u.s_parity;

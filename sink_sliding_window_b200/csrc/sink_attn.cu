@@ -880,15 +880,22 @@ bool launch_chunks(ChunkParams& p, const sink_attn_paged_dims* d, const void* k_
   p.max_parts = static_cast<int>(bound.parts);
   // Units too short to be cut (a window): one wave of CTAs, each taking its
   // turns, which saves every unit the start of a CTA.  Longer ones: a CTA for
-  // each as far as four waves go, which the SMs even out among themselves;
-  // but one wave again when most requests must be single tokens, since the
-  // few-rows kernel can take its place beside this one only when all CTAs of
-  // this one have started.  (Window-128 chunks: 86 us in turns, 92 with a CTA
-  // each; 2048 tokens of 32768: 1493 in turns, 1410; 5 chunks and 28 tokens:
-  // 77 in turns, 87.)
+  // each, which the SMs even out among themselves (as many as whole units come
+  // from the rows, four waves at least: most of the bound for requests' ends is
+  // CTAs that find no work); but one wave again when most requests must be
+  // single tokens, since the few-rows kernel can take its place beside this one
+  // only when all CTAs of this one have started.  (Window-128 chunks: 86 us in
+  // turns, 92 with a CTA each; 2048 tokens of 32768: 1445 in turns, 1383; five
+  // chunks and 28 tokens: 77 in turns, 87.)
   const bool turns = bound.parts == 0 || d->total_tokens < static_cast<int64_t>(d->batch) * d->max_new / 2;
   const int64_t places = bound.units + bound.parts;
-  const unsigned ctas = static_cast<unsigned>(std::min<int64_t>(places, (turns ? 1 : kChunkMaxWaves + 1) * p.wave));
+  // (With one CTA a SM, e4m3, four waves are enough: nobody computes while the
+  // next CTA starts.  Nine prompts of 200 to 3000 tokens: 430 us, 445 with all.
+  // Four of 4096 over bf16: 744 with all, 797 with four waves.)
+  const int64_t whole =
+      kChunkPerSm<kF8> > 1 ? static_cast<int64_t>(p.a.T / (p.tiles * p.tokens)) * p.a.Hkv : 0;  // units, but for requests' ends
+  const unsigned ctas = static_cast<unsigned>(
+      std::min(places, turns ? p.wave : std::max<int64_t>((kChunkMaxWaves + 1) * p.wave, whole)));
   if (bound.parts) *join = static_cast<unsigned>(p.max_cut * (p.tiles * kBlockM / 32));
   return launch_early(sink_attn_paged_chunk_kernel<kF8>, dim3(ctas), kChunkThreads<kF8>, chunk_smem_bytes<kF8>(), st, tm_q,
                       tm_k, tm_v, p);
