@@ -166,13 +166,22 @@ void fill(sink_attn_paged_dims* d, const Cache& c) {
   d->head_stride = stride_of(*c.k, 2);
 }
 
-// The C call, with the interpreter free for other threads.
+// Frees the interpreter for other threads, and takes it back however the scope
+// is left: an exception is turned into Python's by code that needs it.
+struct Released {
+  PyThreadState* state = PyEval_SaveThread();
+  Released() = default;
+  Released(const Released&) = delete;
+  ~Released() { PyEval_RestoreThread(state); }
+};
+
+// The C call, with the interpreter free for other threads.  What can be refused
+// (an address of a tensor without memory, a number out of range) is worked out
+// before it.
 template <typename F>
 sink_attn_status run(F&& f) {
-  PyThreadState* state = PyEval_SaveThread();
-  const sink_attn_status st = f();
-  PyEval_RestoreThread(state);
-  return st;
+  const Released released;
+  return f();
 }
 
 int* ints(const Tensor& t) { return t.data_ptr<int>(); }
@@ -190,7 +199,8 @@ PyObject* plan(const Args& a) {
   check(table, "block_table", at::kInt, {B, kAny}, dev);
   check(ring, "free_pages", at::kInt, {kAny}, dev);
   check(pool, "pool", at::kInt, {2}, dev);
-  const int64_t max_tokens = a.integer(6, "max_tokens"), window = a.integer(7, "window");
+  const int64_t max_tokens = a.integer(6, "max_tokens");
+  const int window = as_int(a.integer(7, "window"), "window");
   const bool has_first = !a.none(8);
   if (has_first)
     check(a.tensor(8, "first_page"), "first_page", at::kInt, {B}, dev);
@@ -203,6 +213,9 @@ PyObject* plan(const Args& a) {
   d.max_pages = as_int(table.size(1), "max_pages");
   d.page_size = as_int(a.integer(5, "page_size"), "page_size");
   d.num_pages = as_int(ring.numel(), "num_pages");
+  const int *const cached_p = ints(cached), *const fresh_p = ints(fresh), *const pool_p = ints(pool);
+  int *const table_p = ints(table), *const ring_p = ints(ring);
+  const int* const first_p = has_first ? ints(a.tensor(8, "first_page")) : nullptr;
   const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(dev));
   static const char* const names[5] = {"cu_seqlens", "kv_lens", "slot_map", "pool_out", "first_page_out"};
   const int64_t sizes[5] = {B + 1, B, max_tokens, 2, B};
@@ -222,11 +235,11 @@ PyObject* plan(const Args& a) {
     out[3].copy_(pool);
   } else {
     void* const stream = c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(dev)).stream();
-    const int* first = has_first ? ints(a.tensor(8, "first_page")) : nullptr;
+    int* to[5] = {};
+    for (int i = 0; i < outs; ++i) to[i] = ints(out[i]);
     const sink_attn_status st = run([&] {
-      return sink_attn_paged_plan(&d, ints(cached), ints(fresh), ints(table), ints(ring), ints(pool), first,
-                                  as_int(window, "window"), ints(out[0]), ints(out[1]), ints(out[2]), ints(out[3]),
-                                  has_first ? ints(out[4]) : nullptr, stream);
+      return sink_attn_paged_plan(&d, cached_p, fresh_p, table_p, ring_p, pool_p, first_p, window, to[0], to[1], to[2],
+                                  to[3], to[4], stream);
     });
     if (st != SINK_ATTN_OK) return PyLong_FromLong(st);
   }
@@ -254,13 +267,14 @@ PyObject* append(const Args& a) {
   sink_attn_paged_dims d = {};
   d.total_tokens = as_int(T, "tokens");
   fill(&d, c);
+  const void *const k_p = k.data_ptr(), *const v_p = v.data_ptr();
+  const int* const slots_p = ints(slots);
+  void *const kc_p = c.k->data_ptr(), *const vc_p = c.v->data_ptr();
   const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(c.device));
   void* const stream = c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(c.device)).stream();
   const sink_attn_status st = run([&] {
-    return c.codes ? sink_attn_paged_append_e4m3(&d, k.data_ptr(), v.data_ptr(), ks, vs, ints(slots), c.k->data_ptr(),
-                                                 c.v->data_ptr(), c.k_scale, c.v_scale, stream)
-                   : sink_attn_paged_append(&d, k.data_ptr(), v.data_ptr(), ks, vs, ints(slots), c.k->data_ptr(),
-                                            c.v->data_ptr(), stream);
+    return c.codes ? sink_attn_paged_append_e4m3(&d, k_p, v_p, ks, vs, slots_p, kc_p, vc_p, c.k_scale, c.v_scale, stream)
+                   : sink_attn_paged_append(&d, k_p, v_p, ks, vs, slots_p, kc_p, vc_p, stream);
   });
   if (st != SINK_ATTN_OK) return PyLong_FromLong(st);
   return PyTuple_Pack(2, a.object(3), a.object(4));
@@ -288,6 +302,9 @@ PyObject* attn(const Args& a) {
   d.max_pages = as_int(table.size(1), "max_pages");
   d.q_stride = qs;
   fill(&d, c);
+  const void *const q_p = q.data_ptr(), *const kc_p = c.k->data_ptr(), *const vc_p = c.v->data_ptr();
+  const int *const table_p = ints(table), *const cu_p = ints(cu), *const lens_p = ints(lens);
+  const float* const sinks_p = sinks.data_ptr<float>();
   const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(c.device));
   Tensor out, lse, ws;
   if (a.none(12)) {
@@ -311,14 +328,14 @@ PyObject* attn(const Args& a) {
                     ws.device().str());
   }
   void* const stream = c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(c.device)).stream();
+  void *const out_p = out.data_ptr(), *const ws_p = ws.data_ptr();
+  float* const lse_p = lse.data_ptr<float>();
+  const size_t ws_bytes = ws.nbytes();
   const sink_attn_status st = run([&] {
-    float* const s = sinks.data_ptr<float>();
-    return c.codes ? sink_attn_paged_attn_e4m3(&d, q.data_ptr(), c.k->data_ptr(), c.v->data_ptr(), ints(table), ints(cu),
-                                               ints(lens), c.k_scale, c.v_scale, s, window, scale, out.data_ptr(),
-                                               lse.data_ptr<float>(), ws.data_ptr(), ws.nbytes(), stream)
-                   : sink_attn_paged_attn(&d, q.data_ptr(), c.k->data_ptr(), c.v->data_ptr(), ints(table), ints(cu),
-                                          ints(lens), s, window, scale, out.data_ptr(), lse.data_ptr<float>(),
-                                          ws.data_ptr(), ws.nbytes(), stream);
+    return c.codes ? sink_attn_paged_attn_e4m3(&d, q_p, kc_p, vc_p, table_p, cu_p, lens_p, c.k_scale, c.v_scale, sinks_p,
+                                               window, scale, out_p, lse_p, ws_p, ws_bytes, stream)
+                   : sink_attn_paged_attn(&d, q_p, kc_p, vc_p, table_p, cu_p, lens_p, sinks_p, window, scale, out_p,
+                                          lse_p, ws_p, ws_bytes, stream);
   });
   if (st != SINK_ATTN_OK) return PyLong_FromLong(st);
   PyObject* o = a.none(12) ? THPVariable_Wrap(std::move(out)) : Py_NewRef(a.object(12));
