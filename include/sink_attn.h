@@ -370,6 +370,9 @@ int sink_attn_decode_launches(const sink_attn_decode_dims* dims, int window);
  *     table row.  A request that needs pages when those left do not suffice
  *     gets none, nor does any request behind it that needs some: its slots are
  *     -1, its kv_lens stays cached_lens, and device error 0x202 is recorded.
+ *     So it is with a request whose tokens do not fit its table row (0x204).
+ *     Its rows keep their places in cu_seqlens (whose sums end at 2^31 - 1),
+ *     and what attention writes into them means nothing.
  *   - An ended request gives back its pages (from first_page on); its kv_lens
  *     and first_page_out become 0.
  *   - With window > 0 (needs first_page) a request gives back the pages wholly

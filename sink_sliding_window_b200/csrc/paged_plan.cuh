@@ -5,7 +5,8 @@
 // With c = cached_lens[b], n = new_lens[b] (negative: the request has ended)
 // and P = page_size:
 //   held = ceil(c / P), need = ceil((c + n) / P) - held
-//   cu_seqlens = exclusive prefix sum of max(n, 0)
+//   cu_seqlens = exclusive prefix sum of max(n, 0), of refused requests too: the
+//   caller packed their rows, and those behind them lie where that puts them
 //   the k-th new page of request b is free_pages[(head + sum_{a<b} need_a + k) mod N]
 //   slot of the token at position p = page(p / P) * P + p mod P
 //   released: all of an ended request's pages; with a window, the pages that
@@ -56,6 +57,12 @@ constexpr size_t plan_smem_bytes(int batch) { return (4 * static_cast<size_t>(ba
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
+// Sum of two counts of tokens, at most 2^31 - 1 (so it can be taken in any order):
+// what a caller asks for may be more than 32 bits count, and a slot map ends far before.
+__device__ __forceinline__ int plan_add(int a, int b) {
+  return static_cast<int>(min(static_cast<uint32_t>(a) + static_cast<uint32_t>(b), 0x7fffffffu));
+}
+
 // Largest i in [0, n) with v[i] <= x, for non-decreasing v with v[0] <= x.
 __device__ __forceinline__ int plan_find(const int* v, int n, int x) {
   int lo = 0, hi = n - 1;
@@ -100,7 +107,7 @@ __global__ void __launch_bounds__(kPlanThreads) sink_attn_paged_plan_kernel(cons
     const bool fine = c >= 0 && (ended ? c : static_cast<int64_t>(c) + n) <= most;
     bad_ |= !fine;
     kv_[i] = ended ? 0 : c;
-    n_[i] = ended ? 0 : static_cast<int>(min(static_cast<int64_t>(n), most));
+    n_[i] = ended ? 0 : n;
     c = static_cast<int>(min(static_cast<int64_t>(max(c, 0)), most));
     const int held = static_cast<int>((static_cast<int64_t>(c) + p.page_size - 1) >> p.page_log2);
     const int low = min(max(low_in, 0), held);
@@ -115,7 +122,7 @@ __global__ void __launch_bounds__(kPlanThreads) sink_attn_paged_plan_kernel(cons
     }
     s_len[b] = c;
     s_page[b] = fine && !ended ? 0 : -1;
-    sum_n += n_[i];
+    sum_n = plan_add(sum_n, n_[i]);
     sum_need += need_[i];
     sum_rel += rel_[i];
   }
@@ -126,8 +133,10 @@ __global__ void __launch_bounds__(kPlanThreads) sink_attn_paged_plan_kernel(cons
   for (int o = 1; o < 32; o <<= 1) {
     const int a = __shfl_up_sync(0xffffffffu, in_n, o), b = __shfl_up_sync(0xffffffffu, in_need, o),
               c = __shfl_up_sync(0xffffffffu, in_rel, o);
-    if (lane >= o) in_n += a, in_need += b, in_rel += c;
+    if (lane >= o) in_n = plan_add(in_n, a), in_need += b, in_rel += c;
   }
+  int before_n = __shfl_up_sync(0xffffffffu, in_n, 1);  // (a cut sum has no difference)
+  if (lane == 0) before_n = 0;
   if (lane == 31) s_sum[0][warp] = in_n, s_sum[1][warp] = in_need, s_sum[2][warp] = in_rel;
   if (tid == 0) s_taken = 0;
   __syncthreads();
@@ -136,13 +145,13 @@ __global__ void __launch_bounds__(kPlanThreads) sink_attn_paged_plan_kernel(cons
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int a = __shfl_up_sync(0xffffffffu, v, o);
-      if (lane >= o) v += a;
+      if (lane >= o) v = plan_add(v, a);
     }
     s_sum[warp][lane] = v;
   }
   __syncthreads();
   const int total = s_sum[0][31], released = s_sum[2][31];
-  int at_n = in_n - sum_n + (warp ? s_sum[0][warp - 1] : 0);
+  int at_n = plan_add(before_n, warp ? s_sum[0][warp - 1] : 0);
   int at_need = in_need - sum_need + (warp ? s_sum[1][warp - 1] : 0);
   int at_rel = in_rel - sum_rel + (warp ? s_sum[2][warp - 1] : 0);
   bool dry = false;
@@ -165,7 +174,7 @@ __global__ void __launch_bounds__(kPlanThreads) sink_attn_paged_plan_kernel(cons
         dry = true;
       }
     }
-    at_n += n_[i];
+    at_n = plan_add(at_n, n_[i]);
     at_need += need_[i];
     at_rel += rel_[i];
   }
@@ -180,9 +189,7 @@ __global__ void __launch_bounds__(kPlanThreads) sink_attn_paged_plan_kernel(cons
   // Tokens: slot_map and, at a page's first token, the table entry.
   const int step = static_cast<int>(gridDim.x) * kPlanThreads;
   const int self = static_cast<int>(blockIdx.x) * kPlanThreads + tid;
-  const int64_t tokens = max(total, p.max_tokens);
-  for (int64_t t64 = self; t64 < tokens; t64 += step) {
-    const int t = static_cast<int>(t64);
+  for (int t = self; t < p.max_tokens; t += step) {
     int slot = -1;
     if (t < total) {
       const int b = plan_find(s_cu, p.batch, t);
@@ -203,7 +210,18 @@ __global__ void __launch_bounds__(kPlanThreads) sink_attn_paged_plan_kernel(cons
         else atomicCAS(&g_device_error, 0, static_cast<int>(kDevErrBadPage));
       }
     }
-    if (t < p.max_tokens) p.slots[t] = slot;
+    p.slots[t] = slot;
+  }
+  // Tokens that the slot map has no room for (reported above) take their pages all the same.
+  if (total > p.max_tokens) {
+    for (int b = self; b < p.batch; b += step) {
+      if (s_page[b] < 0) continue;
+      const int held = (s_len[b] + p.page_size - 1) >> p.page_log2;
+      const int end = (s_len[b] + p.fresh[b] + p.page_size - 1) >> p.page_log2;
+      for (int j = held; j < end; ++j)
+        p.table[static_cast<int64_t>(b) * p.max_pages + j] =
+            p.ring[(static_cast<int64_t>(head) + s_page[b] + j - held) % num];
+    }
   }
   // Released pages, in the order of the requests and of their pages.
   for (int r = self; r < released; r += step) {
