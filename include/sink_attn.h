@@ -377,8 +377,9 @@ int sink_attn_decode_launches(const sink_attn_decode_dims* dims, int window);
  *     and first_page_out become 0.
  *   - With window > 0 (needs first_page) a request gives back the pages wholly
  *     before position cached_lens - window + 1, which no query of this step or
- *     a later one sees.  Pages given back go to the tail of the ring, in the
- *     order of requests and pages; this step takes none of them.
+ *     a later one sees, also when its new tokens get no room.  Pages given back
+ *     go to the tail of the ring, in the order of requests and pages; this step
+ *     takes none of them.
  *   - slot_map[t] is the slot of packed token t, and -1 from the last token on
  *     up to max_tokens.
  *   - kv_lens may be cached_lens, pool_out may be pool and first_page_out may

@@ -104,7 +104,8 @@ __global__ void __launch_bounds__(kPlanThreads) sink_attn_paged_plan_kernel(cons
     const int n = p.fresh[b];
     const int low_in = p.first ? p.first[b] : 0;
     const bool ended = n < 0;
-    const bool fine = c >= 0 && (ended ? c : static_cast<int64_t>(c) + n) <= most;
+    const bool known = c >= 0 && c <= most;  // the row can hold the tokens that it says it has
+    const bool fine = known && (ended || static_cast<int64_t>(c) + n <= most);
     bad_ |= !fine;
     kv_[i] = ended ? 0 : c;
     n_[i] = ended ? 0 : n;
@@ -115,7 +116,9 @@ __global__ void __launch_bounds__(kPlanThreads) sink_attn_paged_plan_kernel(cons
       rel_[i] = held - low;
     } else {
       int drop = low;
-      if (p.window > 0 && fine) drop = max(low, max(0, c - p.window + 1) >> p.page_log2);
+      // By the tokens it has, whether or not the new ones fit: a request at the end
+      // of its row would otherwise hold pages that nobody sees until it ends.
+      if (p.window > 0 && known) drop = max(low, max(0, c - p.window + 1) >> p.page_log2);
       rel_[i] = drop - low;
       drop_[i] = drop;
       if (fine) need_[i] = static_cast<int>((static_cast<int64_t>(c) + n + p.page_size - 1) >> p.page_log2) - held;

@@ -107,3 +107,24 @@ def test_pages_of_tokens_behind_the_slot_map(max_tokens):
     got = _run(cached, new, table, ring, [0, 300], page, max_tokens)
     _expect(got, plan(cached, new, table, ring, [0, 300], page, max_tokens))
     assert got["error"] == (0x204 if sum(new) > max_tokens else 0)
+
+
+@pytest.mark.parametrize("window,gone", [(1, 4), (16, 3), (17, 3), (18, 2), (40, 1), (48, 1), (49, 1), (50, 0), (200, 0)])
+@pytest.mark.parametrize("first", [0, 2])
+def test_a_full_row_gives_back_what_its_window_leaves(window, gone, first):
+    """A request whose row of 64 tokens is full and that asks for one more is
+    refused, and gives back the pages wholly before its window all the same
+    (position 64 - window + 1 is the first that anyone sees)."""
+    page = 16
+    table = [[0, 1, 2, 3], [4, 5, -1, -1]]
+    for b in range(first):
+        table[0][b] = -1
+    back = list(range(first, max(first, gone)))
+    other = 1 if window == 1 else 0  # the other request's first page, which it gave back before
+    got = _run([64, 17], [1, 20], table, [6, 7] + [-1] * 6, [0, 2], page, 21, window, [first, other])
+    assert got["error"] == 0x204 and got["kv"] == [64, 37] and got["cu"] == [0, 1, 21]
+    assert got["slots"][:2] == [-1, 5 * page + 1]
+    assert got["first"] == [max(first, gone), other]
+    assert got["table"] == [table[0], [4, 5, 6, -1]]
+    assert got["ring"] == [6, 7] + back + [-1] * (6 - len(back))
+    assert got["pool"] == [1, 1 + len(back)]
