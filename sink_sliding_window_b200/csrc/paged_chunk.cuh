@@ -64,7 +64,7 @@ struct ChunkParams {
   float* part_o;       // [part][kTiles * 128 rows][64]
   float2* part_ml;     // [part][kTiles * 128] (m in log2 units, l)
   int4* part_unit;     // [cut unit] (request, unit within its head, head, parts)
-  int* part_units;     // cut units of this call
+  int2* part_units;    // cut units of this call, parts of each
 };
 
 // One round's work: a unit, or a part of it.
@@ -245,7 +245,7 @@ __global__ void __launch_bounds__(kChunkThreads<kF8>, kChunkPerSm<kF8>)
       const int full = total / p.wave * p.wave, rest = total - full;
       int parts = p.part_o && rest ? chunk_parts(rest, static_cast<int>(all_steps / total), p.wave) : 1;
       if (rest > p.max_cut || rest * parts > p.max_parts) parts = 1;
-      if (blockIdx.x == 0 && p.part_units) *p.part_units = parts > 1 ? rest : 0;
+      if (blockIdx.x == 0 && p.part_units) *p.part_units = make_int2(parts > 1 ? rest : 0, parts);
       ctl->total = total;
       ctl->full = parts > 1 ? full : total;
       ctl->parts = parts;

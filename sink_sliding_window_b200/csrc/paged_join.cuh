@@ -3,6 +3,7 @@
 // launch costs as much as the work.
 #pragma once
 #include "paged_chunk.cuh"
+#include "paged_cut.cuh"
 #include "paged_rows.cuh"
 
 namespace sa {
@@ -129,9 +130,16 @@ __device__ __forceinline__ void rows_join(const PagedParams& p, RowsJoinSmem& sm
 // The parts of the chunk kernel's i-th cut unit, and the sink, for 32 of its
 // rows: half a warp per row, four dims per lane.
 __device__ __forceinline__ void chunk_join(const ChunkParams& p, int i, int rows32) {
-  if (i >= __ldcg(p.part_units)) return;
+  const int2 cut = __ldcg(p.part_units);
+  if (i >= cut.x) return;
   const int4 u = __ldcg(p.part_unit + i);
-  const PagedRequest rq = paged_request(p.a, u.x);
+  PagedRequest rq;
+  const int unit_tokens = p.tiles * p.tokens;
+  if (!cut_unit_fits(u.x, u.y, u.z, u.w, p.a.batch, p.a.Hkv, cut.y, [&](int b) {
+        rq = paged_request(p.a, b);
+        return rq.n > p.a.few ? (rq.n + unit_tokens - 1) / unit_tokens : 0;
+      }))
+    return;
   const int d = threadIdx.x & 15;
 #pragma unroll
   for (int x = 0; x < 2; ++x) {

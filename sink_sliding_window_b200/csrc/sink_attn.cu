@@ -768,7 +768,7 @@ PagedWorkspace paged_workspace(const sink_attn_paged_dims* d, const PagedSplit& 
     // (Rows of parts: for either type of cache.)
     const size_t rows = static_cast<size_t>(std::max(chunk_bound<false>(d, s, 0).parts * kChunkTiles<false>,
                                                      chunk_bound<true>(d, s, 0).parts * kChunkTiles<true>)) * kBlockM;
-    w.chunk_units = take(sizeof(int));
+    w.chunk_units = take(sizeof(int2));
     w.chunk_unit = take(kChunkPerSm<false> * kChunkSms * sizeof(int4));
     w.chunk_ml = take(rows * sizeof(float2));
     w.chunk_o = take(rows * kHeadDim * sizeof(float));
@@ -961,7 +961,7 @@ sink_attn_status paged_attn_impl(const sink_attn_paged_dims* d, const void* q, c
   if (split.chunks) {
     c.a = p;
     c.tokens = kBlockM / p.G;
-    c.part_units = reinterpret_cast<int*>(base + ws.chunk_units);
+    c.part_units = reinterpret_cast<int2*>(base + ws.chunk_units);
     c.part_unit = reinterpret_cast<int4*>(base + ws.chunk_unit);
     c.part_ml = reinterpret_cast<float2*>(base + ws.chunk_ml);
     c.part_o = reinterpret_cast<float*>(base + ws.chunk_o);
