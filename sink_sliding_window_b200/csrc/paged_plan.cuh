@@ -189,6 +189,11 @@ __global__ void __launch_bounds__(kPlanThreads) sink_attn_paged_plan_kernel(cons
   }
   __syncthreads();
 
+  // The i-th new page of the step, i < count.
+  auto new_page = [&](int i) {
+    const int at = head + i;  // below 2 num <= 2^28
+    return p.ring[at < num ? at : at - num];
+  };
   // Tokens: slot_map and, at a page's first token, the table entry.
   const int step = static_cast<int>(gridDim.x) * kPlanThreads;
   const int self = static_cast<int>(blockIdx.x) * kPlanThreads + tid;
@@ -204,7 +209,7 @@ __global__ void __launch_bounds__(kPlanThreads) sink_attn_paged_plan_kernel(cons
         int* entry = p.table + static_cast<int64_t>(b) * p.max_pages + j;
         int page;
         if (j >= held) {
-          page = p.ring[(static_cast<int64_t>(head) + s_page[b] + j - held) % num];
+          page = new_page(s_page[b] + j - held);
           if ((pos & (p.page_size - 1)) == 0) *entry = page;
         } else {
           page = *entry;
@@ -222,8 +227,7 @@ __global__ void __launch_bounds__(kPlanThreads) sink_attn_paged_plan_kernel(cons
       const int held = (s_len[b] + p.page_size - 1) >> p.page_log2;
       const int end = (s_len[b] + p.fresh[b] + p.page_size - 1) >> p.page_log2;
       for (int j = held; j < end; ++j)
-        p.table[static_cast<int64_t>(b) * p.max_pages + j] =
-            p.ring[(static_cast<int64_t>(head) + s_page[b] + j - held) % num];
+        p.table[static_cast<int64_t>(b) * p.max_pages + j] = new_page(s_page[b] + j - held);
     }
   }
   // Released pages, in the order of the requests and of their pages.
