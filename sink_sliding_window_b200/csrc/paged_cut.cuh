@@ -14,12 +14,15 @@
 
 namespace sa {
 
-// An entry {request, unit within its head, head, parts}; units(b): units of
-// request b, which may be asked for once b is known to be one.
-template <typename Units>
+// An entry {request, unit within its head, head, parts}; rows(b): tokens of
+// request b, 0 if none of them are in units of `unit` tokens, which may be
+// asked for once b is known to be a request.  (A product, not a division: the
+// join's CTAs do little else than wait, and a division took them 1 us of 49.)
+template <typename Rows>
 SINK_ATTN_HOST_DEVICE bool cut_unit_fits(int b, int group, int head, int parts, int batch, int heads, int call_parts,
-                                         Units units) {
-  return b >= 0 && b < batch && head >= 0 && head < heads && parts == call_parts && group >= 0 && group < units(b);
+                                         int unit, Rows rows) {
+  return b >= 0 && b < batch && head >= 0 && head < heads && parts == call_parts && group >= 0 &&
+         static_cast<long long>(group) * unit < rows(b);
 }
 
 }  // namespace sa

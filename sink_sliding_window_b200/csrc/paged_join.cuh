@@ -134,10 +134,9 @@ __device__ __forceinline__ void chunk_join(const ChunkParams& p, int i, int rows
   if (i >= cut.x) return;
   const int4 u = __ldcg(p.part_unit + i);
   PagedRequest rq;
-  const int unit_tokens = p.tiles * p.tokens;
-  if (!cut_unit_fits(u.x, u.y, u.z, u.w, p.a.batch, p.a.Hkv, cut.y, [&](int b) {
+  if (!cut_unit_fits(u.x, u.y, u.z, u.w, p.a.batch, p.a.Hkv, cut.y, p.tiles * p.tokens, [&](int b) {
         rq = paged_request(p.a, b);
-        return rq.n > p.a.few ? (rq.n + unit_tokens - 1) / unit_tokens : 0;
+        return rq.n > p.a.few ? rq.n : 0;
       }))
     return;
   const int d = threadIdx.x & 15;

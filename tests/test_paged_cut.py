@@ -19,7 +19,8 @@ PROGRAM = r"""
 struct Call {
   int batch, heads, parts, cut, G, tokens, tiles, T, max_parts;
   int cu[6];
-  int units(int b) const { const int u = tiles * tokens; return (cu[b + 1] - cu[b] + u - 1) / u; }
+  int rows(int b) const { return cu[b + 1] - cu[b]; }
+  int units(int b) const { return (rows(b) + tiles * tokens - 1) / (tiles * tokens); }
   bool inside(int i, int b, int group, int head, int n) const {
     if (b < 0 || b >= batch) return false;  // cu, kv_lens
     for (int k = 0; k < n; ++k)             // parts of the workspace
@@ -40,21 +41,21 @@ int main() {
   std::mt19937 rng(1);
   const int odd[] = {0, 1, 2, 3, 4, 5, 6, 31, 32, 33, 128, -1, -2, 1 << 24, 1 << 30, INT_MAX, INT_MIN, 0x5A5A5A5A, 0x7FC00000};
   long long taken = 0, refused = 0, wrong = 0, lost = 0;
-  auto units = [&](int b) {
+  auto rows = [&](int b) {
     if (b < 0 || b >= c.batch) ++wrong;  // asked for a request that there is not
-    return b >= 0 && b < c.batch ? c.units(b) : 0;
+    return b >= 0 && b < c.batch ? c.rows(b) : 0;
   };
   for (int x = 0; x < 400000; ++x) {
     int e[4];
     for (int& v : e) v = rng() % 4 ? odd[rng() % (sizeof(odd) / sizeof(int))] : static_cast<int>(rng());
-    const bool fits = sa::cut_unit_fits(e[0], e[1], e[2], e[3], c.batch, c.heads, c.parts, units);
+    const bool fits = sa::cut_unit_fits(e[0], e[1], e[2], e[3], c.batch, c.heads, c.parts, 32, rows);
     (fits ? taken : refused) += 1;
     if (fits && !c.inside(c.cut - 1, e[0], e[1], e[2], e[3])) ++wrong;
   }
   for (int b = 0; b < c.batch; ++b)
     for (int u = 0; u < c.units(b); ++u)
       for (int h = 0; h < c.heads; ++h)
-        if (!sa::cut_unit_fits(b, u, h, c.parts, c.batch, c.heads, c.parts, units)) ++lost;
+        if (!sa::cut_unit_fits(b, u, h, c.parts, c.batch, c.heads, c.parts, 32, rows)) ++lost;
   std::printf("%lld %lld %lld %lld\n", taken, refused, wrong, lost);
 }
 """
