@@ -13,7 +13,6 @@ struct PagedParams {
   int page_log2, num_pages, max_pages;
   int box_log2;      // tokens of one TMA box of the few-rows kernel
   int few;           // a request of at most this many new tokens goes to the few-rows kernel
-  bool beside;       // few-rows kernel: the chunk kernel runs before it on the stream
   int window;        // 0: full causal
   float scale_log2;  // scale * log2(e)
   long long q_stride;
@@ -37,9 +36,16 @@ struct PagedParams {
   int4* part_unit;   // [workers] (b or -1, chunk, begins, 0)
 };
 
-// All loads of a call's inputs are plain ones: the kernels may start while the
-// ones before them still write (see pdl_wait), which rules out the read-only
-// path.
+// Loads of a call's inputs.  The kernels may start while the ones before them
+// still write (see pdl_wait), which rules out the read-only path.  kL2: through
+// L2, where those writes are once they are done; the few-rows kernel beside a
+// chunk kernel never executes that wait before it reads, so nothing promises it
+// that the L1 of its SM holds no older copy.  (Everywhere, that cost short
+// decode steps 2 or 3%.)
+template <bool kL2 = false, typename T>
+__device__ __forceinline__ T paged_load(const T* at) {
+  return kL2 ? __ldcg(at) : *at;
+}
 
 // One request's rows and keys.  Lengths that do not fit the call's sizes are
 // cut to them (and reported by paged_check), so that no index leaves a tensor.
@@ -49,25 +55,28 @@ struct PagedRequest {
   int lo;      // first key that any of its rows sees; the last one is len - 1
 };
 
+template <bool kL2 = false>
 __device__ __forceinline__ PagedRequest paged_request(const PagedParams& p, int b) {
   PagedRequest r;
-  r.t0 = min(max(*(p.cu + b), 0), p.T);
-  r.n = min(max(*(p.cu + b + 1), r.t0), p.T) - r.t0;
-  r.len = min(max(*(p.kv_lens + b), 0), p.max_pages << p.page_log2);
+  r.t0 = min(max(paged_load<kL2>(p.cu + b), 0), p.T);
+  r.n = min(max(paged_load<kL2>(p.cu + b + 1), r.t0), p.T) - r.t0;
+  r.len = min(max(paged_load<kL2>(p.kv_lens + b), 0), p.max_pages << p.page_log2);
   r.lo = p.window > 0 ? max(0, r.len - r.n - p.window + 1) : 0;
   return r;
 }
 
 // Reports a request whose lengths do not fit.
+template <bool kL2 = false>
 __device__ __forceinline__ void paged_check(const PagedParams& p, int b) {
-  const int c0 = *(p.cu + b), c1 = *(p.cu + b + 1), len = *(p.kv_lens + b);
+  const int c0 = paged_load<kL2>(p.cu + b), c1 = paged_load<kL2>(p.cu + b + 1), len = paged_load<kL2>(p.kv_lens + b);
   if (c0 < 0 || c1 < c0 || c1 > p.T || c1 - c0 > p.max_new || len < 0 || len > (p.max_pages << p.page_log2))
     atomicCAS(&g_device_error, 0, static_cast<int>(kDevErrPagedRows));
 }
 
 // The table's entry for the page that holds key j of request b.
+template <bool kL2 = false>
 __device__ __forceinline__ int paged_entry(const PagedParams& p, int b, int j) {
-  return *(p.table + static_cast<long long>(b) * p.max_pages + (j >> p.page_log2));
+  return paged_load<kL2>(p.table + static_cast<long long>(b) * p.max_pages + (j >> p.page_log2));
 }
 
 // A table entry as a page: num_pages, which a TMA load reads as zeros, when it

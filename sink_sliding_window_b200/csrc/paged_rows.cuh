@@ -171,7 +171,8 @@ struct RowsAxis {
   }
 };
 
-template <bool kF8, int kR>
+// kBeside: the chunk kernel of the same call runs before it on the stream.
+template <bool kF8, int kR, bool kBeside>
 __global__ void __launch_bounds__(kRowsThreads, 1)
     sink_attn_paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                                 const __grid_constant__ PagedParams p) {
@@ -204,7 +205,9 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
   }
   // The call's inputs and the workspace are free to use; beside the chunk
   // kernel they are already, since that waited before it let this one start.
-  if (!p.beside) pdl_wait();
+  // What that wait saw finished lies in L2, and there this kernel reads it
+  // (paged_load, and TMA).
+  if (!kBeside) pdl_wait();
   pdl_launch_dependents();
   // pre[]: every CTA sums the requests' blocks for itself.
   {
@@ -214,8 +217,8 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
     for (int i = 0; i < per; ++i) {
       const int b = b0 + i;
       if (b >= p.batch) break;
-      if (blockIdx.x == 0) paged_check(p, b);
-      const int n = rows_blocks<kF8>(p, paged_request(p, b));
+      if (blockIdx.x == 0) paged_check<kBeside>(p, b);
+      const int n = rows_blocks<kF8>(p, paged_request<kBeside>(p, b));
       pre[b + 1] = n;
       sum += n;
       live += n > 0;
@@ -267,6 +270,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
   const uint32_t group_bytes = p.per_chunk * stages * 2 * kTile, stage_bytes = p.per_chunk * 2 * kTile;
   if (warp == kWarps) {
     // ------------------------------------------------------------------ copies
+    if (kBeside) fence_proxy_async_global();
     // Lanes lpg * g .. of the warp keep the state of worker g and, one per
     // box, the page numbers of a batch of its next blocks; the batch after it
     // is looked up while this one is copied.
@@ -282,14 +286,14 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
     auto look_up = [&]() {
       Batch t = {0, 0, 0, 0, false};
       if (left == 0) return t;
-      const PagedRequest r = paged_request(p, at.b);
+      const PagedRequest r = paged_request<kBeside>(p, at.b);
       const int blocks = axis.blocks(at.b);
       t.n = min(min(lpg / nbox, blocks - at.off), left);
       t.c = at.c;
       t.key = rows_first(p, r) + at.off * kKeys;
       const int j = t.key + (li << p.box_log2);
       t.want = li < t.n * nbox && j < r.len;
-      if (t.want) t.entry = paged_entry(p, at.b, j);
+      if (t.want) t.entry = paged_entry<kBeside>(p, at.b, j);
       left -= t.n;
       at.off += t.n;
       if (at.off == blocks) axis.next_unit(at);
@@ -358,7 +362,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
     if (reports) p.part_unit[worker] = unit;
     return;
   }
-  PagedRequest rq = paged_request(p, at.b);
+  PagedRequest rq = paged_request<kBeside>(p, at.b);
   int first = rows_first(p, rq), blocks = axis.blocks(at.b);
   const uint8_t* ring = smem + group * group_bytes;
   uint64_t *full = ctl->full + group * stages, *empty = ctl->empty + group * stages;
@@ -385,7 +389,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
       whole = at.off == 0;
       g = min(at.c * p.per_chunk + hw, p.Hkv - 1);
       real = at.c * p.per_chunk + hw < p.Hkv;
-      sl2 = kF8 ? p.scale_log2 * *(p.k_scale + g) : p.scale_log2;
+      sl2 = kF8 ? p.scale_log2 * paged_load<kBeside>(p.k_scale + g) : p.scale_log2;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         m[h] = -INFINITY;
@@ -401,12 +405,12 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
           uint32_t a = 0u, c = 0u;
           if (h < kHalves && t < rq.n) {
             if constexpr (kF8) {
-              const uint2 v = *(reinterpret_cast<const uint2*>(src + 16 * kk + 4 * t4));
+              const uint2 v = paged_load<kBeside>(reinterpret_cast<const uint2*>(src + 16 * kk + 4 * t4));
               a = bf16x2_to_f16x2_sat(v.x);
               c = bf16x2_to_f16x2_sat(v.y);
             } else {
-              a = *(reinterpret_cast<const uint32_t*>(src + 16 * kk + 2 * t4));
-              c = *(reinterpret_cast<const uint32_t*>(src + 16 * kk + 8 + 2 * t4));
+              a = paged_load<kBeside>(reinterpret_cast<const uint32_t*>(src + 16 * kk + 2 * t4));
+              c = paged_load<kBeside>(reinterpret_cast<const uint32_t*>(src + 16 * kk + 8 + 2 * t4));
             }
           }
           q[kk][h] = a;
@@ -550,7 +554,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
       const bool begun = whole;
       whole = whole && unit_end;
       const int slot = (2 * worker + (unit_end ? 0 : 1)) * per_group + in_group;
-      const float vs = kF8 ? *(p.v_scale + g) : 1.f;
+      const float vs = kF8 ? paged_load<kBeside>(p.v_scale + g) : 1.f;
 #pragma unroll
       for (int h = 0; h < kHalves; ++h) {
         const int row = row0 + 8 * h + r8;
@@ -562,7 +566,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
         const int head = valid ? g * p.G + row - t * p.G : 0;
         float f = vs;
         if (whole) {
-          const float s2 = *(p.sinks + head) * kLog2e;
+          const float s2 = paged_load<kBeside>(p.sinks + head) * kLog2e;
           const float top = fmaxf(s2, m[h]);
           float all = 0.f;
           f = 0.f;
@@ -610,7 +614,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
         axis.next_unit(at);
         if (at.b != last) {
           blocks = axis.blocks(at.b);
-          rq = paged_request(p, at.b);
+          rq = paged_request<kBeside>(p, at.b);
           first = rows_first(p, rq);
         }
       }

@@ -811,19 +811,19 @@ bool rows_never_cut(const PagedParams& p) {
   return (keys + lead + kRowsKeys<kF8> - 1) / kRowsKeys<kF8> <= 2 * kRowsSnap<kF8> + 1;
 }
 
-// `beside`: the chunk kernel runs before it on the stream.  The two share
+// kBeside: the chunk kernel runs before it on the stream.  The two share
 // nothing but the SMs, which take the pieces of this kernel as they run out of
 // chunks, so it does not wait for the other to end.
-template <bool kF8, int kR>
-bool launch_rows(PagedParams& p, const sink_attn_paged_dims* d, const void* k_cache, const void* v_cache, bool beside,
-                 dim3* join, cudaStream_t st) {
+template <bool kF8, int kR, bool kBeside>
+bool launch_rows(PagedParams& p, const sink_attn_paged_dims* d, const void* k_cache, const void* v_cache, dim3* join,
+                 cudaStream_t st) {
   const int box = std::min(d->page_size, kRowsKeys<kF8>);
   p.box_log2 = ilog2_exact(box);
   CUtensorMap tm_k, tm_v;
   if (!make_map_paged(&tm_k, k_cache, d, kF8, box, p.per_chunk) ||
       !make_map_paged(&tm_v, v_cache, d, kF8, box, p.per_chunk)) return false;
   static SmemAttrOnce smem_set;
-  if (!smem_set.ensure(sink_attn_paged_rows_kernel<kF8, kR>, rows_smem_bytes(kPagedMaxBatch))) return false;
+  if (!smem_set.ensure(sink_attn_paged_rows_kernel<kF8, kR, kBeside>, rows_smem_bytes(kPagedMaxBatch))) return false;
   const bool cut = !rows_never_cut<kF8>(p);
   if (!cut) p.part_unit = nullptr;
   // No more CTAs than the most blocks there can be give work to.
@@ -834,9 +834,15 @@ bool launch_rows(PagedParams& p, const sink_attn_paged_dims* d, const void* k_ca
   const int per_group = p.per_chunk * p.row_parts, groups = kRowsWarps / per_group;
   const int ctas = static_cast<int>(std::min<int64_t>(kPagedCtas, workers));
   if (cut) *join = dim3(ctas * groups, per_group);
-  p.beside = beside;
-  return launch_early(sink_attn_paged_rows_kernel<kF8, kR>, dim3(ctas), kRowsThreads, rows_smem_bytes(p.batch), st, tm_k,
+  return launch_early(sink_attn_paged_rows_kernel<kF8, kR, kBeside>, dim3(ctas), kRowsThreads, rows_smem_bytes(p.batch), st, tm_k,
                       tm_v, p);
+}
+
+template <bool kF8, int kR>
+bool launch_rows(PagedParams& p, const sink_attn_paged_dims* d, const void* k_cache, const void* v_cache, bool beside,
+                 dim3* join, cudaStream_t st) {
+  return beside ? launch_rows<kF8, kR, true>(p, d, k_cache, v_cache, join, st)
+                : launch_rows<kF8, kR, false>(p, d, k_cache, v_cache, join, st);
 }
 
 template <bool kF8>
@@ -933,7 +939,6 @@ sink_attn_status paged_attn_impl(const sink_attn_paged_dims* d, const void* q, c
   p.max_pages = d->max_pages;
   p.box_log2 = 0;
   p.few = split.few;
-  p.beside = false;
   p.row_parts = split.row_parts;
   p.chunks = rows_chunks(d, split);
   p.per_chunk = (p.Hkv + p.chunks - 1) / p.chunks;

@@ -19,24 +19,29 @@ def _code(name):
     return re.sub(r"//[^\n]*", "", text)
 
 
-@pytest.mark.parametrize("name", ["paged_attn.cuh", "paged_rows.cuh"])
-def test_inputs_are_read_through_l2(name):
+@pytest.mark.parametrize("name,load", [("paged_attn.cuh", "paged_load<kL2>("), ("paged_rows.cuh", "paged_load<kBeside>(")])
+def test_inputs_are_read_through_l2(name, load):
     code = _code(name)
     for field in INPUTS:
         for m in re.finditer(rf"\bp\.{field}\b(?!\s*=[^=])", code):
             before = code[:m.start()]
             line = before[before.rfind(";") + 1:] + code[m.start():code.index(";", m.start())]
             # Either loaded by paged_load or made into an address that is (q's rows).
-            assert "paged_load(" in before[before.rfind(";") + 1:] or "src =" in line, line.strip()
+            assert load in before[before.rfind(";") + 1:] or "src =" in line, line.strip()
             assert f"p.{field}[" not in line and not re.search(rf"(?<![\w)])\*\s*\(?p\.{field}\b", line), line.strip()
     for m in re.finditer(r"\bsrc \+ 16", code):  # and nothing but paged_load follows such an address
-        assert "paged_load(" in code[code[:m.start()].rfind("=") + 1:m.start()]
+        assert load in code[code[:m.start()].rfind("=") + 1:m.start()]
 
 
-def test_loads_through_l2_are_loads_through_l2():
+def test_the_kernel_asks_for_it_everywhere():
+    code = _code("paged_rows.cuh")
+    calls = re.findall(r"\b(paged_(?:request|check|entry|load))(<\w+>)?\(", code)
+    assert len(calls) >= 12 and all(t == "<kBeside>" for _, t in calls), calls
     body = _code("paged_attn.cuh")
     body = body[body.index("paged_load("):]
-    assert "__ldcg(at)" in body[:body.index("}")]
+    assert "kL2 ? __ldcg(at)" in body[:body.index("}")]
+    launch = _code("sink_attn.cu")
+    assert "beside ? launch_rows<kF8, kR, true>" in launch
 
 
 KINDS = pytest.mark.parametrize("e4m3", [False, True], ids=["bf16", "e4m3"])
