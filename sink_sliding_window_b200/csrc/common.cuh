@@ -48,14 +48,6 @@ __device__ __forceinline__ int first_key(const Geometry& g, int t) {
   return g.window > 0 ? max(a, t - g.window + 1) : a;
 }
 
-// Programmatic dependent launch.  A kernel launched so may start while the one
-// before it on the stream runs, as soon as all CTAs of that one have allowed it
-// (launch_dependents) or ended; pdl_wait() returns when that one and all before
-// it have ended and what they wrote can be read.  Without such a launch both do
-// nothing.
-__device__ __forceinline__ void pdl_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
 // Rounds a dynamic shared-memory pointer up to 1024 bytes (128B-swizzled
 // tiles must start on a 1024-byte boundary).
 __device__ __forceinline__ uint8_t* align1024(uint8_t* p) {

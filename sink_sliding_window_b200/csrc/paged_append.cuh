@@ -3,6 +3,7 @@
 // e4m3 codes.  A pure copy, bound by HBM: every byte is read and written once.
 #pragma once
 #include "decode_kernel.cuh"
+#include "paged_base.cuh"
 
 namespace sa {
 

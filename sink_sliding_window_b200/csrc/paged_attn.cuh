@@ -2,6 +2,7 @@
 // keys of one request.
 #pragma once
 #include "decode_kernel.cuh"
+#include "paged_base.cuh"
 
 namespace sa {
 

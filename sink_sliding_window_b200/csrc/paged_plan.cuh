@@ -24,7 +24,7 @@
 // cluster separates the reads of the lengths from the writes of their
 // successors, which may be the same arrays.
 #pragma once
-#include "common.cuh"
+#include "paged_base.cuh"
 
 namespace sa {
 

@@ -23,10 +23,6 @@ enum DeviceError : int {
   // A decode query needs a key whose cache slot already holds a newer
   // token (the ring is smaller than window + new tokens - 1).
   kDevErrDecodeCacheTooSmall = 0x201,
-  kDevErrPoolExhausted = 0x202,  // a planned step wanted more pages than the pool holds
-  kDevErrBadPage = 0x203,        // a needed block-table entry, pool entry or slot lies outside the pool
-  kDevErrPlanLengths = 0x204,    // a request's lengths do not fit its table row, or the step its slot map
-  kDevErrPagedRows = 0x205,      // cu_seqlens do not fit total_tokens, or a request has more than max_new tokens
 };
 
 // One second: far beyond any legitimate wait in these kernels.
@@ -175,12 +171,6 @@ __device__ __forceinline__ void bulk_wait_group() {
 // proxy (TMA, tensor cores).
 __device__ __forceinline__ void fence_proxy_async_smem() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-}
-
-// Orders this thread's generic-proxy view of global memory before its later TMA
-// copies from there.
-__device__ __forceinline__ void fence_proxy_async_global() {
-  asm volatile("fence.proxy.async.global;" ::: "memory");
 }
 
 // Barrier over `count` threads (a multiple of 32) on hardware barrier `id`.
