@@ -479,11 +479,13 @@ sink_attn_status sink_attn_paged_attn_e4m3(const sink_attn_paged_dims* dims,
 const char* sink_attn_status_string(sink_attn_status s);
 
 /* Synchronises `stream` (a cudaStream_t passed as void*), then returns and
- * clears the device error code that a timed-out wait (or a decode ring too
- * small for its window) recorded on the current device: 0 = none, -1 = the
- * synchronisation or the read failed.  These are the only entry points that
- * synchronise.  sink_attn_device_error is the same function under a shorter
- * name. */
+ * clears a device error code recorded on the current device: 0 = none, -1 = the
+ * synchronisation or the read failed.  There are two records, of the first wait
+ * that timed out (0x1..) and of the first input that a kernel found wrong
+ * (0x2..: a decode ring too small for its window, a pool that ran dry and so
+ * on); a time-out is returned first, and the other by the call after that.
+ * These are the only entry points that synchronise.  sink_attn_device_error is
+ * the same function under a shorter name. */
 int sink_attn_last_device_error(void* stream);
 int sink_attn_device_error(void* stream);
 

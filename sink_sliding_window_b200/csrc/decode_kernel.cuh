@@ -47,6 +47,7 @@
 #include <cuda_fp16.h>
 
 #include "common.cuh"
+#include "input_error.cuh"
 
 namespace sa {
 
@@ -371,7 +372,7 @@ __global__ void __launch_bounds__(kMode ? kDecThreads8 : kDecThreads, (kMode && 
     mbar_init(&ctl->pv_done[1], 1);
     mbar_init(&ctl->o_full, 1);
     ctl->abort = 0;
-    if (w.bad) atomicCAS(&g_device_error, 0, static_cast<int>(kDevErrDecodeCacheTooSmall));
+    if (w.bad) report_input(kDevErrDecodeCacheTooSmall);
     fence_mbar_init();
   }
   if (threadIdx.x < kDecRows) {

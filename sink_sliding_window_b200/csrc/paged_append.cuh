@@ -37,7 +37,7 @@ __global__ void __launch_bounds__(256) sink_attn_paged_append_kernel(const Appen
   const int slot = *(p.slots + t);
   if (slot < 0) return;  // padding, or a request without room
   if (slot >= p.slots_end) {
-    atomicCAS(&g_device_error, 0, static_cast<int>(kDevErrBadPage));
+    report_input(kDevErrBadPage);
     return;
   }
   const uint4* ks = reinterpret_cast<const uint4*>(p.k_new + t * p.k_stride + g * kHeadDim + c * 16);

@@ -71,7 +71,7 @@ template <bool kL2 = false>
 __device__ __forceinline__ void paged_check(const PagedParams& p, int b) {
   const int c0 = paged_load<kL2>(p.cu + b), c1 = paged_load<kL2>(p.cu + b + 1), len = paged_load<kL2>(p.kv_lens + b);
   if (c0 < 0 || c1 < c0 || c1 > p.T || c1 - c0 > p.max_new || len < 0 || len > (p.max_pages << p.page_log2))
-    atomicCAS(&g_device_error, 0, static_cast<int>(kDevErrPagedRows));
+    report_input(kDevErrPagedRows);
 }
 
 // The table's entry for the page that holds key j of request b.
@@ -84,7 +84,7 @@ __device__ __forceinline__ int paged_entry(const PagedParams& p, int b, int j) {
 // lies outside the pool.
 __device__ __forceinline__ int paged_page(const PagedParams& p, int entry) {
   if (entry >= 0 && entry < p.num_pages) return entry;
-  atomicCAS(&g_device_error, 0, static_cast<int>(kDevErrBadPage));
+  report_input(kDevErrBadPage);
   return p.num_pages;
 }
 

@@ -3,6 +3,7 @@
 // exactly its sources.)
 #pragma once
 #include "common.cuh"
+#include "input_error.cuh"
 
 namespace sa {
 

@@ -184,8 +184,8 @@ __global__ void __launch_bounds__(kPlanThreads) sink_attn_paged_plan_kernel(cons
   if (taken > 0) atomicMax(&s_taken, taken);
   if (tid == 0) s_cu[p.batch] = total, s_rel[p.batch] = released;
   if (blockIdx.x == 0) {
-    if (bad_ || (tid == 0 && total > p.max_tokens)) atomicCAS(&g_device_error, 0, static_cast<int>(kDevErrPlanLengths));
-    if (dry) atomicCAS(&g_device_error, 0, static_cast<int>(kDevErrPoolExhausted));
+    if (bad_ || (tid == 0 && total > p.max_tokens)) report_input(kDevErrPlanLengths);
+    if (dry) report_input(kDevErrPoolExhausted);
   }
   __syncthreads();
 
@@ -215,7 +215,7 @@ __global__ void __launch_bounds__(kPlanThreads) sink_attn_paged_plan_kernel(cons
           page = *entry;
         }
         if (page >= 0 && page < num) slot = (page << p.page_log2) + (pos & (p.page_size - 1));
-        else atomicCAS(&g_device_error, 0, static_cast<int>(kDevErrBadPage));
+        else report_input(kDevErrBadPage);
       }
     }
     p.slots[t] = slot;

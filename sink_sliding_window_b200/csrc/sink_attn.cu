@@ -259,7 +259,9 @@ int sink_attn_last_device_error(void* stream) {
   if (cudaStreamSynchronize(st) != cudaSuccess) return -1;
   int v = 0, zero = 0;
   if (cudaMemcpyFromSymbol(&v, g_device_error, sizeof(int)) != cudaSuccess) return -1;
-  if (v != 0 && cudaMemcpyToSymbol(g_device_error, &zero, sizeof(int)) != cudaSuccess) return -1;
+  if (v != 0) return cudaMemcpyToSymbol(g_device_error, &zero, sizeof(int)) == cudaSuccess ? v : -1;
+  if (cudaMemcpyFromSymbol(&v, g_input_error, sizeof(int)) != cudaSuccess) return -1;
+  if (v != 0 && cudaMemcpyToSymbol(g_input_error, &zero, sizeof(int)) != cudaSuccess) return -1;
   return v;
 }
 

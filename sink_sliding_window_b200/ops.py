@@ -430,6 +430,10 @@ def paged_attn(q, k_cache, v_cache, block_table, cu_seqlens, kv_lens, sinks, win
 
 
 def device_error(stream=None) -> int:
+    """sink_attn_device_error: synchronises the stream, returns and clears a
+    device error code (0: none).  A wait that ran out comes first; what calls
+    found wrong with their inputs is a record of its own, which the next call
+    returns."""
     return int(load().sink_attn_last_device_error(_stream_handle(stream)))
 
 
