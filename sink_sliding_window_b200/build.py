@@ -1,5 +1,5 @@
 """Builds libsinkattn.so (the C-ABI library) in-tree with nvcc for sm_100a, and
-_paged.so, the native binding of its paged-cache calls.
+the native binding of its paged-cache calls (binding_path()) if torch is there.
 
     python -m sink_sliding_window_b200.build [--force] [--verbose-ptxas]
 """
@@ -17,7 +17,6 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libsinkattn.so")
-BINDING = os.path.join(PKG, "_paged.so")
 BINDING_SRC = os.path.join(CSRC, "paged_binding.cpp")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
@@ -38,24 +37,31 @@ def up_to_date() -> bool:
     return _newer(LIB, _sources())
 
 
-def build_binding(force: bool = False) -> str:
-    """_paged.so: compiled by the host compiler against torch's headers, it
-    finds libsinkattn.so beside it."""
-    header = os.path.join(INCLUDE, "sink_attn.h")
-    if not force and _newer(BINDING, [BINDING_SRC, header]):
-        return BINDING
+def binding_path() -> str:
+    """The native binding's file, which names the interpreter and the torch that
+    it is compiled for: neither promises the next version its binary interface."""
     import torch
+    return os.path.join(PKG, f"_paged.{sys.implementation.cache_tag}.torch-{torch.__version__}.so")
+
+
+def build_binding(force: bool = False) -> str:
+    """The binding, compiled by the host compiler against torch's headers; it
+    finds libsinkattn.so beside it."""
+    import torch
+    target, header = binding_path(), os.path.join(INCLUDE, "sink_attn.h")
+    if not force and _newer(target, [BINDING_SRC, header]):
+        return target
     root = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(NVCC))
-    tmp = BINDING + f".tmp{os.getpid()}"
+    tmp = target + f".tmp{os.getpid()}"
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE,
            "-isystem", os.path.join(root, "include"), "-isystem", os.path.join(cuda, "include"),
            "-isystem", sysconfig.get_paths()["include"], BINDING_SRC, "-o", tmp, "-L", PKG, "-l:" + os.path.basename(LIB),
            "-L", os.path.join(root, "lib"), "-lc10", "-ltorch_cpu", "-ltorch_python", "-lc10_cuda", "-Wl,-rpath,$ORIGIN"]
     subprocess.run(cmd, check=True)
-    os.replace(tmp, BINDING)
-    return BINDING
+    os.replace(tmp, target)
+    return target
 
 
 def build(force: bool = False, ptxas_verbose: bool = False) -> str:
@@ -68,6 +74,10 @@ def build(force: bool = False, ptxas_verbose: bool = False) -> str:
             cmd.insert(1, "-Xptxas=-v")
         subprocess.run(cmd, check=True)
         os.replace(tmp, LIB)
+    try:
+        import torch  # noqa: F401
+    except ImportError:
+        return LIB  # complete for programs in C; the binding is torch's
     build_binding(force)
     return LIB
 

@@ -14,6 +14,8 @@ import os
 
 import torch
 
+from . import build
+
 _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libsinkattn.so")
 _lib = None
 
@@ -351,9 +353,10 @@ def _paged_calls():
     global _paged
     if _paged is None:
         load()
-        path = os.path.join(os.path.dirname(_LIB_PATH), "_paged.so")
+        path = build.binding_path()
         if not os.path.exists(path):
-            raise RuntimeError(f"_paged.so not found at {path}; build it with `python -m sink_sliding_window_b200.build`")
+            raise RuntimeError(f"the paged calls' binding for this torch not found at {path}; build it with "
+                               "`python -m sink_sliding_window_b200.build`")
         spec = importlib.util.spec_from_file_location("_paged", path)
         module = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(module)

@@ -65,3 +65,24 @@ print("then:", cu.tolist(), ops.device_error())
     r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stderr[-2000:]
     assert "refused:" in r.stdout and "then: [0, 1, 2] 0" in r.stdout
+
+
+def test_a_binding_of_another_torch_is_not_loaded(monkeypatch):
+    """Neither found up to date nor loaded: the file names what it is for."""
+    here = build.binding_path()
+    assert torch.__version__ in here and sys.implementation.cache_tag in here
+    assert ops._paged_calls().__file__ == here
+    monkeypatch.setattr(torch, "__version__", "0.0.1")
+    monkeypatch.setattr(ops, "_paged", None)
+    assert build.binding_path() != here
+    with pytest.raises(RuntimeError, match="torch-0.0.1"):
+        ops._paged_calls()
+
+
+def test_the_library_is_built_without_torch():
+    """As before there was a binding: torch is not needed for libsinkattn.so."""
+    code = ("import sys; sys.modules['torch'] = None\n"
+            "from sink_sliding_window_b200 import build\n"
+            "import os; print(os.path.exists(build.build()))")
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True)
+    assert r.returncode == 0 and r.stdout.strip() == "True", r.stderr[-2000:]
