@@ -131,10 +131,11 @@ class Paged:
         each) before they multiply the values, the result once more; the
         fp32 logits, exponentials and sums add less than 1/16 of that:
           2^-8 (|out| + sum_j pi_j |v_j|) * 17/16.
-        Over e4m3 codes the weights are two e4m3 terms, again within 2^-8 of
-        each, or within 2^-22 of the largest weight for those below e4m3's
-        range (doubled here for the largest that a later key raises):
-          + 2^-21 max_j pi_j sum_j |v_j|.
+        Over e4m3 codes the weights are fp16, half a step of which is 2^-11 of
+        each, or 2^-25 of the largest for those below fp16's range.  This
+        bound allows them what bf16 weights have, and
+          + 2^-21 max_j pi_j sum_j |v_j|;
+        test_paged_rounding.py holds them to their own.
         lse: fp32 logits x (64 products of 16-bit numbers, |error| at most
         2^-18 of sum |q_d k_d| scale, the running maximum's rounding and
         ex2's 2^-22 with them): 2^-18 (1 + max_j sum_d |q_d k_d| scale)."""
