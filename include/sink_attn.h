@@ -450,9 +450,13 @@ size_t sink_attn_paged_workspace_size(const sink_attn_paged_dims* dims);
  * as they were.  A row that sees no key gets out = 0 and lse = its sink.
  * G = Hq / Hkv is any whole number up to 128; batch is at most 4096, and batch *
  * max_pages * page_size * Hkv at most 2^35.  q_stride >= Hq * D where T > 1.
- * Requests of up to 64 / G tokens and longer ones go to different kernels, which
- * run side by side; max_new tells which of them a call needs, so a decode step
- * should say 1.  Nothing is read back to the host: the lengths may change
+ * Requests of few tokens and of many go to different kernels, which run side by
+ * side.  Few are up to max_new tokens where max_new * G <= 64, and in calls with
+ * longer requests up to 8 / G, one at least (none for G > 64).  So max_new tells
+ * which kernels a call needs, and with batch and T whether its chunks come among
+ * mostly single tokens, which are shared out in another way: a decode step should
+ * say 1, and a step of prompts its longest one (three or more of them with
+ * max_new = T take up to a tenth longer).  Nothing is read back to the host: the lengths may change
  * between replays of a captured call.  `workspace`: caller-owned, 256-byte
  * aligned, of sink_attn_paged_workspace_size(dims) bytes and any content; calls
  * whose execution may overlap need one each.  T = 0 or batch = 0 is a no-op. */

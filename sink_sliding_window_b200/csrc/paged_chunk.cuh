@@ -21,6 +21,10 @@
 // of V are zeroed in shared memory by the softmax threads of the steps that
 // hold such keys, since 0 * NaN is not 0.
 //
+// Rounding: P to bf16 over a bf16 cache, as the forward (both operands of an MMA
+// have one type; half a step is 2^-8 of a weight), to fp16 over codes; the rest
+// is fp32.
+//
 // e4m3: the codes come by TMA into a ring of 4 KB slots, and two warps write
 // them widened to fp16 (exactly) into the same tiles that TMA fills for bf16.
 // Widening costs as much for two query tiles as for four, so one CTA of four

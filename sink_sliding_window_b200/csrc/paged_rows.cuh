@@ -34,6 +34,10 @@
 // -inf, not at the sink: a sink far above the logits would push every weight
 // below the range of fp16.
 //
+// Rounding over a bf16 cache: P to bf16, since the two operands of an MMA have
+// one type and V is bf16; half a step is 2^-8 of each weight.  l sums the weights
+// before that, and S, m, l and O are fp32.
+//
 // e4m3: K and V are widened to fp16 (exactly) in registers, between ldmatrix
 // and mma.  A 16-bit ldmatrix element is two codes, so a thread gets four
 // neighbouring dims of a key where the instruction wants two and two: the dims

@@ -894,7 +894,9 @@ bool launch_chunks(ChunkParams& p, const sink_attn_paged_dims* d, const void* k_
   // single tokens, since the few-rows kernel can take its place beside this one
   // only when all CTAs of this one have started.  (Window-128 chunks: 61 us in
   // turns, 84 with a CTA each; 2048 tokens of 32768: 1445 in turns, 1383; five
-  // chunks and 28 tokens: 76 in turns, 85.)
+  // chunks and 28 tokens: 76 in turns, 85.  A call that leaves max_new at T and
+  // has three requests or more counts as single tokens: four prompts of 4096 take
+  // 826 to 837 us then, 754 to 768 with max_new given.)
   const bool turns = bound.parts == 0 || d->total_tokens < static_cast<int64_t>(d->batch) * d->max_new / 2;
   const int64_t places = bound.units + bound.parts;
   // (With one CTA a SM, e4m3, four waves are enough: nobody computes while the

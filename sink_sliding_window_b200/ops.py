@@ -417,7 +417,10 @@ def paged_attn(q, k_cache, v_cache, block_table, cu_seqlens, kv_lens, sinks, win
     attend over the pages of k_cache / v_cache [num_pages, page_size, Hkv, D]
     that block_table int32 [B, max_pages] names.  cu_seqlens int32 [B + 1],
     kv_lens int32 [B] (tokens after the step, the new ones included), sinks
-    [Hq] fp32.  max_new bounds the new tokens of one request (default T).
+    [Hq] fp32.  max_new bounds the new tokens of one request (default T); the
+    call is planned by it, so give it where it is known: a decode step of one
+    token each left at T goes through both kernels, and three or more prompts
+    take up to a tenth longer.
     Returns (out [T, Hq, D], lse [Hq, T]); rows behind cu_seqlens[B] are left
     as they were."""
     args = (q, k_cache, v_cache, block_table, cu_seqlens, kv_lens, sinks, window, scale, max_new, k_scale, v_scale, out,
