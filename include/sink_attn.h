@@ -456,10 +456,11 @@ size_t sink_attn_paged_workspace_size(const sink_attn_paged_dims* dims);
  * which kernels a call needs, and with batch and T whether its chunks come among
  * mostly single tokens, which are shared out in another way: a decode step should
  * say 1, and a step of prompts its longest one (three or more of them with
- * max_new = T take up to a tenth longer).  Nothing is read back to the host: the lengths may change
- * between replays of a captured call.  `workspace`: caller-owned, 256-byte
- * aligned, of sink_attn_paged_workspace_size(dims) bytes and any content; calls
- * whose execution may overlap need one each.  T = 0 or batch = 0 is a no-op. */
+ * max_new = T take up to a tenth longer).  Nothing is read back to the host: the
+ * lengths may change between replays of a captured call.  `workspace`:
+ * caller-owned, 256-byte aligned, of sink_attn_paged_workspace_size(dims) bytes
+ * and any content; calls whose execution may overlap need one each.  T = 0 or
+ * batch = 0 is a no-op. */
 sink_attn_status sink_attn_paged_attn(const sink_attn_paged_dims* dims,
                                       const void* q, const void* k_cache, const void* v_cache,
                                       const int* block_table, const int* cu_seqlens, const int* kv_lens,
